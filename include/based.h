@@ -22,8 +22,9 @@
  *     linear attention over the KV/K states, and a `window`-slot ring cache).
  *
  * Beside it: the layer's per-head input projections and the BaseConv block
- * (tensor-core GEMM with fused epilogues), and the gradients of both
- * attention layers (CUDA cores).
+ * (tensor-core GEMM with fused epilogues), the gradients of both attention
+ * layers, and the operators around a mixer: layer norm, rotary positions and a
+ * gated recurrence, with their gradients.
  *
  * Conventions shared by every entry point
  *   - All tensor pointers are DEVICE pointers, owned by the caller, C-contiguous
@@ -295,6 +296,154 @@ based_status_t based_baseconv_fwd(const void* x, const void* w, const float* bia
                                   based_dtype_t dt, based_stream_t stream);
 
 /*
+ * Layer norm over the last axis, with the add of the residual stream
+ * (the "based/train" README builds its layers with a fused layer norm):
+ *   r = x + residual, rounded to dt   (r = x when residual is NULL)
+ *   m = mean(r), s = 1 / sqrt(mean((r - m)^2) + eps), y = (r - m) s weight + bias
+ *   x, residual, y, resid_out  [rows, D]  dt     weight, bias [D] fp32
+ *   residual  may be NULL; resid_out receives r and is given exactly when
+ *             residual is (BASED_ERR_INVALID_ARG otherwise)
+ *   bias      may be NULL (no bias)
+ *   mean, rstd [rows] fp32 or NULL: m and s, for the gradient (written)
+ * The norm is that of the stream as it is stored (rounded), so the gradient of
+ * the stored stream is the gradient of this call.  eps > 0, 1 <= D <= 16384
+ * (else BASED_ERR_UNSUPPORTED), any number of rows.  In place: resid_out may be
+ * x or residual, and y may be the other of them (or x); no other overlap.
+ */
+based_status_t based_layernorm_fwd(const void* x, const void* residual, const float* weight,
+                                   const float* bias, void* y, void* resid_out, float* mean,
+                                   float* rstd, long long rows, int D, based_dtype_t dt, float eps,
+                                   based_stream_t stream);
+
+/*
+ * Gradient of based_layernorm_fwd with respect to r (which is also that of x and
+ * of residual), weight and bias, given dy and the gradient that reaches the
+ * stored stream from elsewhere:
+ *   xh = (r - m) s, t = weight dy:  dx = s (t - mean(t) - xh mean(t xh)) + dresid
+ *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy
+ *   dy, x [rows, D] dt (x is r: the forward's resid_out, or its x)
+ *   mean, rstd [rows] fp32, from the forward
+ *   dresid [rows, D] fp32 or NULL;  dx [rows, D] fp32 (written; may be dresid)
+ *   dweight, dbias [D] fp32 (written; dbias may be NULL)
+ *   workspace: based_layernorm_bwd_workspace_bytes() bytes of device memory on
+ *   the CURRENT device (BASED_ERR_WORKSPACE if smaller), contents are scratch.
+ * The sums over rows are taken in a fixed order: equal calls on a device give
+ * equal bits.  rows = 0 zeroes dweight and dbias.
+ */
+size_t based_layernorm_bwd_workspace_bytes(long long rows, int D);
+based_status_t based_layernorm_bwd(const void* dy, const void* x, const float* weight,
+                                   const float* mean, const float* rstd, const float* dresid,
+                                   float* dx, float* dweight, float* dbias, long long rows, int D,
+                                   based_dtype_t dt, void* workspace, size_t workspace_bytes,
+                                   based_stream_t stream);
+
+/* Which values of a head form a pair: (i, i + rot_dim/2) or (2i, 2i + 1). */
+typedef enum { BASED_ROTARY_HALF = 0, BASED_ROTARY_INTERLEAVED = 1 } based_rotary_layout_t;
+/* How the frequencies are changed for a context longer than the trained one. */
+typedef enum {
+    BASED_ROTARY_NONE = 0,
+    BASED_ROTARY_LINEAR = 1,   /* every frequency divided by factor */
+    BASED_ROTARY_BY_PARTS = 2  /* only the pairs that turn slowly, see below */
+} based_rotary_scaling_t;
+
+/*
+ * Fills a HOST array of rot_dim/2 doubles with the turns per position of each
+ * pair (a host function; nothing is launched).  Copy it to the device once.
+ *   f_i = base^(-2i / rot_dim) / (2 pi)
+ *   BASED_ROTARY_LINEAR:    f_i / factor
+ *   BASED_ROTARY_BY_PARTS:  n_i = f_i original_len (turns over the trained
+ *     context), keep_i = clamp((n_i - low_turns) / (high_turns - low_turns), 0, 1),
+ *     f_i (keep_i + (1 - keep_i) / factor)
+ * base > 0, factor >= 1, original_len >= 1, high_turns > low_turns, all finite
+ * (BASED_ERR_INVALID_ARG otherwise; arguments that the scaling does not use are
+ * not looked at).
+ */
+based_status_t based_rotary_freqs(double* freqs, int rot_dim, double base,
+                                  based_rotary_scaling_t scaling, double factor,
+                                  long long original_len, double low_turns, double high_turns);
+
+/*
+ * Rotary positions of queries and keys in one launch (the "based/train" README
+ * lists a rotary kernel among those its attention layers use):
+ * pair i of the head at position p, with angle 2 pi p freqs[i],
+ *   (u, v) -> mscale (u cos - v sin, u sin + v cos);
+ * values from rot_dim on are copied.
+ *   q, q_out [B, H_q, L, D] dt;  k, k_out [B, H_k, L, D] dt (outputs written)
+ *   q or k may be left out (NULL with H_q or H_k = 0)
+ *   freqs    [rot_dim/2] fp64, DEVICE memory, turns per position (see above)
+ *   pos      DEVICE array of B int64 (8-byte aligned): token t of sequence b is
+ *            at position pos[b] + t; NULL: at pos0 + t for every sequence
+ * 2 <= rot_dim <= D, even.  Positions lie in [0, 2^31): pos0 outside is refused
+ * (negative: BASED_ERR_INVALID_ARG, too large: BASED_ERR_UNSUPPORTED); an entry of
+ * pos outside is found by the kernel, which leaves that sequence's outputs
+ * untouched and records BASED_ERR_INVALID_ARG (based_get_device_error).
+ * In place (q_out = q, k_out = k) is allowed; no other overlap.
+ */
+based_status_t based_rotary_fwd(const void* q, const void* k, void* q_out, void* k_out,
+                                const double* freqs, const long long* pos, long long pos0, int B,
+                                int H_q, int H_k, int L, int D, int rot_dim,
+                                based_rotary_layout_t layout, float mscale, based_dtype_t dt,
+                                based_stream_t stream);
+
+/*
+ * Gradient of based_rotary_fwd: the gradients of its outputs (fp32, as
+ * based_window_attn_bwd writes them) turned back, times mscale.  Same arguments;
+ * in place allowed.
+ */
+based_status_t based_rotary_bwd(const float* dq_out, const float* dk_out, float* dq, float* dk,
+                                const double* freqs, const long long* pos, long long pos0, int B,
+                                int H_q, int H_k, int L, int D, int rot_dim,
+                                based_rotary_layout_t layout, float mscale,
+                                based_stream_t stream);
+
+/* Tokens between two states that based_gatedrec_fwd keeps for the gradient. */
+#define BASED_GATEDREC_CHUNK 64
+
+/*
+ * Gated linear recurrence, channel by channel: a mixer with a learned decay
+ * (the "based/train" README explores a decay without giving a formula):
+ *   a_t = sigmoid(g_t),  h_t = a_t h_{t-1} + (1 - a_t) x_t,  y_t = h_t
+ * The gate is given as its logit: bf16 has no value between 0.996 and 1.  A
+ * logit of -inf starts anew from x_t, +inf keeps the state.
+ *   x, g, y   [B, L, D] dt (y written)
+ *   h0        [B, D] fp32 or NULL (zero): the state before the first token
+ *   h_last    [B, D] fp32 or NULL: the state after the last token (written; may
+ *             be h0)
+ *   h_chunks  [B, ceil(L / 64), D] fp32 or NULL: the states that enter tokens 0,
+ *             64, 128, ..., for the gradient (written)
+ *   lengths   DEVICE array of B int64 (8-byte aligned) or NULL: sequence b has
+ *             lengths[b] of the L tokens.  Nothing is read past them; y and
+ *             h_chunks are written as zero there.  An entry outside [0, L] is found
+ *             by the kernel: that sequence's outputs are left untouched and
+ *             BASED_ERR_INVALID_ARG is recorded (based_get_device_error).
+ * The state is fp32 throughout.  L = 0: h_last = h0.
+ */
+based_status_t based_gatedrec_fwd(const void* x, const void* g, void* y, const float* h0,
+                                  float* h_last, float* h_chunks, const long long* lengths, int B,
+                                  int L, int D, based_dtype_t dt, based_stream_t stream);
+
+/*
+ * Gradient of based_gatedrec_fwd: l_t = dy_t + a_{t+1} l_{t+1} (dh_last enters at
+ * the last token), dx_t = (1 - a_t) l_t, dg_t = l_t (h_{t-1} - x_t) a_t (1 - a_t),
+ * dh0 = a_0 l_0.
+ *   x, g, dy [B, L, D] dt;  h_chunks as the forward wrote it (it holds h0)
+ *   dh_last  [B, D] fp32 or NULL (zero);  dh0 [B, D] fp32 or NULL (written; may be dh_last)
+ *   dx, dg   [B, L, D] fp32 (written; zero past a sequence's length)
+ *   lengths  as in the forward
+ */
+based_status_t based_gatedrec_bwd(const void* x, const void* g, const void* dy,
+                                  const float* h_chunks, const float* dh_last, float* dx, float* dg,
+                                  float* dh0, const long long* lengths, int B, int L, int D,
+                                  based_dtype_t dt, based_stream_t stream);
+
+/*
+ * One token of the gated recurrence: x, g, y [B, D] dt; h [B, D] fp32 updated in
+ * place, h = a h + (1 - a) x, and y = h rounded.
+ */
+based_status_t based_gatedrec_step(const void* x, const void* g, float* h, void* y, int B, int D,
+                                   based_dtype_t dt, based_stream_t stream);
+
+/*
  * Test hook for the failure path of the bounded waits; not for production use.
  * Synchronises the current device, then sets, for every later launch on it:
  *   which = 0  normal operation;
@@ -315,8 +464,9 @@ based_status_t based_debug_stall(int which, long long wait_limit_ns);
  * Synchronise `stream`, then read and clear the library's device status word
  * on the current device.  Returns BASED_OK, or the first error a kernel
  * recorded since the last call (BASED_ERR_TIMEOUT; BASED_ERR_INVALID_ARG for a
- * negative position given to based_decode_step_at), or BASED_ERR_CUDA if the
- * synchronisation itself failed.
+ * negative position given to based_decode_step_at, a position out of range given
+ * to the rotary calls or a length out of range given to the gated recurrence), or
+ * BASED_ERR_CUDA if the synchronisation itself failed.
  */
 based_status_t based_get_device_error(based_stream_t stream);
 

@@ -37,6 +37,10 @@ EXPORTED_SYMBOLS = ("based_abi_version", "based_binary_version", "based_status_s
                     "based_proj_heads_fwd", "based_proj_heads_multi_fwd", "based_baseconv_fwd",
                     "based_linattn_bwd_workspace_bytes", "based_linattn_bwd",
                     "based_window_attn_bwd_workspace_bytes", "based_window_attn_bwd",
+                    "based_layernorm_fwd", "based_layernorm_bwd_workspace_bytes",
+                    "based_layernorm_bwd", "based_rotary_freqs", "based_rotary_fwd",
+                    "based_rotary_bwd", "based_gatedrec_fwd", "based_gatedrec_bwd",
+                    "based_gatedrec_step",
                     "based_debug_stall", "based_get_device_error")
 
 
@@ -50,6 +54,7 @@ _lock = threading.Lock()
 _lib = None
 _vp, _fp = ctypes.c_void_p, ctypes.POINTER(ctypes.c_float)
 _i, _f, _ll, _sz = ctypes.c_int, ctypes.c_float, ctypes.c_longlong, ctypes.c_size_t
+_d = ctypes.c_double
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -93,13 +98,25 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.based_proj_heads_multi_fwd.argtypes = [_vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i,
                                                    _vp]
         lib.based_baseconv_fwd.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp]
+        lib.based_layernorm_fwd.argtypes = [_vp] * 8 + [_ll, _i, _i, _f, _vp]
+        lib.based_layernorm_bwd_workspace_bytes.argtypes = [_ll, _i]
+        lib.based_layernorm_bwd_workspace_bytes.restype = _sz
+        lib.based_layernorm_bwd.argtypes = [_vp] * 9 + [_ll, _i, _i, _vp, _sz, _vp]
+        lib.based_rotary_freqs.argtypes = [_vp, _i, _d, _i, _d, _ll, _d, _d]
+        lib.based_rotary_fwd.argtypes = [_vp] * 6 + [_ll] + [_i] * 7 + [_f, _i, _vp]
+        lib.based_rotary_bwd.argtypes = [_vp] * 6 + [_ll] + [_i] * 7 + [_f, _vp]
+        lib.based_gatedrec_fwd.argtypes = [_vp] * 7 + [_i] * 4 + [_vp]
+        lib.based_gatedrec_bwd.argtypes = [_vp] * 9 + [_i] * 4 + [_vp]
+        lib.based_gatedrec_step.argtypes = [_vp] * 4 + [_i] * 3 + [_vp]
         lib.based_get_device_error.argtypes = [_vp]
         lib.based_debug_stall.argtypes = [_i, _ll]
         for name in ("based_linattn_fwd", "based_linattn_fwd_noalloc", "based_window_attn_fwd",
                      "based_window_ring_fill", "based_decode_step", "based_decode_step_at",
                      "based_proj_heads_fwd", "based_proj_heads_multi_fwd",
                      "based_baseconv_fwd", "based_linattn_bwd", "based_window_attn_bwd",
-                     "based_debug_stall", "based_get_device_error"):
+                     "based_layernorm_fwd", "based_layernorm_bwd", "based_rotary_freqs",
+                     "based_rotary_fwd", "based_rotary_bwd", "based_gatedrec_fwd",
+                     "based_gatedrec_bwd", "based_gatedrec_step", "based_debug_stall", "based_get_device_error"):
             getattr(lib, name).restype = _i
         _lib = lib
         return lib
@@ -473,6 +490,232 @@ def based_baseconv_fwd(x, w, bias, taps, y, stream=None):
     return y
 
 
+def _arg(t, shape, dtype, name: str, device: torch.device):
+    """Pointer of a tensor that must have exactly this shape and dtype, be
+    contiguous and sit on this device (None stays None)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr() or None
+
+
+def _required(**ts):
+    for name, t in ts.items():
+        if t is None:
+            raise TypeError(f"{name}: expected a torch.Tensor")
+
+
+def based_layernorm_fwd(x, weight, bias, y, eps: float = 1e-5, residual=None, resid_out=None,
+                        mean=None, rstd=None, stream=None):
+    """y = layer norm of r = x (+ residual) over the last axis, times weight
+    (+ bias).  x, y, residual, resid_out [..., D]; weight, bias [D] float32; mean,
+    rstd float32 of x's leading shape (written if given, for the gradient)."""
+    _required(x=x, weight=weight, y=y)
+    dev = _cuda(_device_of(x))
+    if x.dim() < 1:
+        raise ValueError("x must be [..., D]")
+    shape, dtype = x.shape, x.dtype
+    dt = _dtype_code(x)
+    lead, D = shape[:-1], shape[-1]
+    if (residual is None) != (resid_out is None):
+        raise ValueError("residual and resid_out are given together")
+    f32 = torch.float32
+    args = (_arg(x, shape, dtype, "x", dev), _arg(residual, shape, dtype, "residual", dev),
+            _arg(weight, (D,), f32, "weight", dev), _arg(bias, (D,), f32, "bias", dev),
+            _arg(y, shape, dtype, "y", dev), _arg(resid_out, shape, dtype, "resid_out", dev),
+            _arg(mean, lead, f32, "mean", dev), _arg(rstd, lead, f32, "rstd", dev))
+    with torch.cuda.device(dev):
+        st = load_library().based_layernorm_fwd(*args, lead.numel(), D, dt, float(eps),
+                                                _torch_stream(stream, dev).cuda_stream)
+    _check("based_layernorm_fwd", st)
+    return y
+
+
+def based_layernorm_bwd_workspace_bytes(rows, D) -> int:
+    n = load_library().based_layernorm_bwd_workspace_bytes(int(rows), int(D))
+    if n == ctypes.c_size_t(-1).value:
+        raise BasedError("based_layernorm_bwd_workspace_bytes", 1)
+    return n
+
+
+def based_layernorm_bwd(dy, x, weight, mean, rstd, dx, dweight, dbias, dresid=None,
+                        workspace=None, stream=None):
+    """Gradients (float32, written) of based_layernorm_fwd: dx [..., D] (with
+    dresid added, the gradient that reaches the residual stream from elsewhere),
+    dweight, dbias [D].  x is the normalised stream (resid_out, or x)."""
+    _required(dy=dy, x=x, weight=weight, mean=mean, rstd=rstd, dx=dx, dweight=dweight)
+    dev = _cuda(_device_of(x))
+    if x.dim() < 1:
+        raise ValueError("x must be [..., D]")
+    shape, dtype = x.shape, x.dtype
+    dt = _dtype_code(x)
+    lead, D = shape[:-1], shape[-1]
+    rows = lead.numel()
+    f32 = torch.float32
+    args = (_arg(dy, shape, dtype, "dy", dev), _arg(x, shape, dtype, "x", dev),
+            _arg(weight, (D,), f32, "weight", dev), _arg(mean, lead, f32, "mean", dev),
+            _arg(rstd, lead, f32, "rstd", dev), _arg(dresid, shape, f32, "dresid", dev),
+            _arg(dx, shape, f32, "dx", dev), _arg(dweight, (D,), f32, "dweight", dev),
+            _arg(dbias, (D,), f32, "dbias", dev))
+    ts = _torch_stream(stream, dev)
+    with torch.cuda.device(dev):
+        nbytes = based_layernorm_bwd_workspace_bytes(rows, D) if workspace is None else 0
+        workspace, ws_bytes = _workspace(nbytes, workspace, dev, ts, "based_layernorm_bwd")
+        st = load_library().based_layernorm_bwd(*args, rows, D, dt, _ptr(workspace), ws_bytes,
+                                                ts.cuda_stream)
+    _check("based_layernorm_bwd", st)
+    return dx, dweight, dbias
+
+
+ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
+ROTARY_SCALINGS = {"none": 0, "linear": 1, "by_parts": 2}
+
+
+def based_rotary_freqs(rot_dim: int, base: float = 10000.0, scaling: str = "none",
+                       factor: float = 1.0, original_len: int = 1, low_turns: float = 1.0,
+                       high_turns: float = 4.0) -> torch.Tensor:
+    """Turns per position of each pair, a float64 CPU tensor [rot_dim / 2]."""
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError(f"scaling: one of {sorted(ROTARY_SCALINGS)}, got {scaling!r}")
+    freqs = torch.empty(max(int(rot_dim) // 2, 0), dtype=torch.float64)
+    st = load_library().based_rotary_freqs(freqs.data_ptr() or None, int(rot_dim), float(base),
+                                           ROTARY_SCALINGS[scaling], float(factor),
+                                           int(original_len), float(low_turns), float(high_turns))
+    _check("based_rotary_freqs", st)
+    return freqs
+
+
+def _rotary(fn, q, k, q_out, k_out, freqs, pos, layout, mscale, dtype, stream):
+    ref = q if q is not None else k
+    dev = _cuda(_device_of(ref))
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None):
+        raise ValueError("q and q_out, k and k_out are given together")
+    if ref.dim() != 4:
+        raise ValueError("q, k must be [B, H, L, d_head]")
+    if layout not in ROTARY_LAYOUTS:
+        raise ValueError(f"layout: one of {sorted(ROTARY_LAYOUTS)}, got {layout!r}")
+    B, _, L, D = ref.shape
+    if k is not None and k is not ref and (k.dim() != 4 or k.shape[0] != B or
+                                           k.shape[2:] != ref.shape[2:]):
+        raise ValueError(f"k: expected shape {(B, 'H', L, D)}, got {tuple(k.shape)}")
+    dtype = dtype or ref.dtype
+    dt = _dtype_code(ref)
+    if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
+        raise TypeError("freqs must be a float64 tensor [rot_dim / 2]")
+    per_seq = isinstance(pos, torch.Tensor)
+    H_q, H_k = q.shape[1] if q is not None else 0, k.shape[1] if k is not None else 0
+    args = (_arg(q, ref.shape, dtype, "q", dev), _arg(k, k.shape if k is not None else None,
+                                                      dtype, "k", dev),
+            _arg(q_out, ref.shape, dtype, "q_out", dev),
+            _arg(k_out, k.shape if k is not None else None, dtype, "k_out", dev),
+            _arg(freqs, freqs.shape, torch.float64, "freqs", dev),
+            _arg(pos, (B,), torch.int64, "pos", dev) if per_seq else None,
+            0 if per_seq else int(pos), B, H_q, H_k, L, D, 2 * freqs.shape[0],
+            ROTARY_LAYOUTS[layout], float(mscale))
+    if per_seq and B == 0:
+        return q_out, k_out
+    with torch.cuda.device(dev):
+        handle = _torch_stream(stream, dev).cuda_stream
+        if fn == "based_rotary_fwd":
+            st = load_library().based_rotary_fwd(*args, dt, handle)
+        else:
+            st = load_library().based_rotary_bwd(*args, handle)
+    _check(fn, st)
+    return q_out, k_out
+
+
+def based_rotary_fwd(q, k, q_out, k_out, freqs, pos=0, layout: str = "half",
+                     mscale: float = 1.0, stream=None):
+    """Rotary positions of q [B, H_q, L, d] and k [B, H_k, L, d] (either may be
+    None) into q_out, k_out (which may be q, k).  freqs: float64 CUDA tensor
+    [rot_dim / 2], turns per position (rotary_freqs).  pos: position of the first
+    token, an int or an int64 CUDA tensor [B]."""
+    return _rotary("based_rotary_fwd", q, k, q_out, k_out, freqs, pos, layout, mscale, None,
+                   stream)
+
+
+def based_rotary_bwd(dq_out, dk_out, dq, dk, freqs, pos=0, layout: str = "half",
+                     mscale: float = 1.0, stream=None):
+    """Gradients (float32) of based_rotary_fwd's q, k from those of its outputs
+    (dq may be dq_out, dk may be dk_out)."""
+    return _rotary("based_rotary_bwd", dq_out, dk_out, dq, dk, freqs, pos, layout, mscale,
+                   torch.float32, stream)
+
+
+GATEDREC_CHUNK = 64
+
+
+def _gatedrec_args(x):
+    dev = _cuda(_device_of(x))
+    if x.dim() != 3:
+        raise ValueError("x, g must be [B, L, D]")
+    B, L, D = x.shape
+    return dev, B, L, D, (B, -(-L // GATEDREC_CHUNK), D), _dtype_code(x)
+
+
+def based_gatedrec_fwd(x, g, y, h0=None, h_last=None, h_chunks=None, lengths=None, stream=None):
+    """y_t = h_t = a_t h_{t-1} + (1 - a_t) x_t, a = sigmoid(g): x, g, y [B, L, D];
+    h0, h_last [B, D] float32; h_chunks [B, ceil(L / 64), D] float32 (written, for
+    the gradient); lengths int64 CUDA tensor [B]."""
+    _required(x=x, g=g, y=y)
+    dev, B, L, D, chunks, dt = _gatedrec_args(x)
+    f32 = torch.float32
+    args = (_arg(x, x.shape, x.dtype, "x", dev), _arg(g, x.shape, x.dtype, "g", dev),
+            _arg(y, x.shape, x.dtype, "y", dev), _arg(h0, (B, D), f32, "h0", dev),
+            _arg(h_last, (B, D), f32, "h_last", dev), _arg(h_chunks, chunks, f32, "h_chunks", dev),
+            _arg(lengths, (B,), torch.int64, "lengths", dev))
+    with torch.cuda.device(dev):
+        st = load_library().based_gatedrec_fwd(*args, B, L, D, dt,
+                                               _torch_stream(stream, dev).cuda_stream)
+    _check("based_gatedrec_fwd", st)
+    return y
+
+
+def based_gatedrec_bwd(x, g, dy, h_chunks, dx, dg, dh_last=None, dh0=None, lengths=None,
+                       stream=None):
+    """Gradients (float32, written) of based_gatedrec_fwd given dy and, if the
+    final state was used, dh_last; h_chunks is what the forward wrote."""
+    _required(x=x, g=g, dy=dy, h_chunks=h_chunks, dx=dx, dg=dg)
+    dev, B, L, D, chunks, dt = _gatedrec_args(x)
+    f32 = torch.float32
+    args = (_arg(x, x.shape, x.dtype, "x", dev), _arg(g, x.shape, x.dtype, "g", dev),
+            _arg(dy, x.shape, x.dtype, "dy", dev), _arg(h_chunks, chunks, f32, "h_chunks", dev),
+            _arg(dh_last, (B, D), f32, "dh_last", dev), _arg(dx, x.shape, f32, "dx", dev),
+            _arg(dg, x.shape, f32, "dg", dev), _arg(dh0, (B, D), f32, "dh0", dev),
+            _arg(lengths, (B,), torch.int64, "lengths", dev))
+    with torch.cuda.device(dev):
+        st = load_library().based_gatedrec_bwd(*args, B, L, D, dt,
+                                               _torch_stream(stream, dev).cuda_stream)
+    _check("based_gatedrec_bwd", st)
+    return dx, dg, dh0
+
+
+def based_gatedrec_step(x, g, h, y, stream=None):
+    """One token: h [B, D] float32 becomes a h + (1 - a) x (in place), y [B, D] = h."""
+    _required(x=x, g=g, h=h, y=y)
+    dev = _cuda(_device_of(x))
+    if x.dim() != 2:
+        raise ValueError("x, g must be [B, D]")
+    B, D = x.shape
+    dt = _dtype_code(x)
+    args = (_arg(x, x.shape, x.dtype, "x", dev), _arg(g, x.shape, x.dtype, "g", dev),
+            _arg(h, x.shape, torch.float32, "h", dev), _arg(y, x.shape, x.dtype, "y", dev))
+    with torch.cuda.device(dev):
+        st = load_library().based_gatedrec_step(*args, B, D, dt,
+                                                _torch_stream(stream, dev).cuda_stream)
+    _check("based_gatedrec_step", st)
+    return y
+
+
 STALL_NONE, STALL_LINATTN_V, STALL_WINDOW_V = 0, 1, 2
 
 
@@ -555,3 +798,95 @@ def window_grad(q, k, v, dy, window: int = 64, stream=None):
     """(dq, dk, dv) in float32 for the window attention's output gradient dy."""
     dq, dk, dv = (torch.empty(t.shape, dtype=torch.float32, device=t.device) for t in (q, k, v))
     return based_window_attn_bwd(q, k, v, dy, dq, dk, dv, window, stream=stream)
+
+
+def _new(shape, dtype, device, ts):
+    """An output allocated on the launch stream: memory that another stream's
+    pending work still uses is not handed out for it."""
+    with torch.cuda.stream(ts):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def layernorm(x, weight, bias=None, eps: float = 1e-5, residual=None, return_stats: bool = False,
+              stream=None):
+    """Layer norm of x, or of r = x + residual: y, or (y, r); with return_stats
+    also mean and rstd (float32), for layernorm_grad."""
+    dev = _cuda(_device_of(x))
+    ts = _torch_stream(stream, dev)
+    y = _new(x.shape, x.dtype, dev, ts)
+    r = _new(x.shape, x.dtype, dev, ts) if residual is not None else None
+    mean = rstd = None
+    if return_stats:
+        mean, rstd = (_new(x.shape[:-1], torch.float32, dev, ts) for _ in range(2))
+    based_layernorm_fwd(x, weight, bias, y, eps, residual, r, mean, rstd, stream=ts)
+    out = (y,) + ((r,) if r is not None else ()) + ((mean, rstd) if return_stats else ())
+    return out if len(out) > 1 else y
+
+
+def layernorm_grad(dy, x, weight, mean, rstd, dresid=None, stream=None):
+    """(dx, dweight, dbias) in float32; x is the normalised stream."""
+    dev = _cuda(_device_of(x))
+    ts = _torch_stream(stream, dev)
+    dx = _new(x.shape, torch.float32, dev, ts)
+    dw, db = (_new(x.shape[-1:], torch.float32, dev, ts) for _ in range(2))
+    return based_layernorm_bwd(dy, x, weight, mean, rstd, dx, dw, db, dresid, stream=ts)
+
+
+def rotary_freqs(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                 original_len: int = 1, low_turns: float = 1.0, high_turns: float = 4.0,
+                 device="cuda"):
+    """The frequency table of rotary and rotary_grad (float64, made once)."""
+    return based_rotary_freqs(rot_dim, base, scaling, factor, original_len, low_turns,
+                              high_turns).to(device)
+
+
+def rotary(q, k, freqs, pos=0, layout: str = "half", mscale: float = 1.0, stream=None):
+    """(q, k) with rotary positions (either may be None)."""
+    ref = q if q is not None else k
+    dev = _cuda(_device_of(ref))
+    ts = _torch_stream(stream, dev)
+    qo, ko = (None if t is None else _new(t.shape, t.dtype, dev, ts) for t in (q, k))
+    return based_rotary_fwd(q, k, qo, ko, freqs, pos, layout, mscale, stream=ts)
+
+
+def rotary_grad(dq_out, dk_out, freqs, pos=0, layout: str = "half", mscale: float = 1.0,
+                stream=None):
+    """(dq, dk) in float32 from the gradients of rotary's outputs."""
+    ref = dq_out if dq_out is not None else dk_out
+    dev = _cuda(_device_of(ref))
+    ts = _torch_stream(stream, dev)
+    dq, dk = (None if t is None else _new(t.shape, torch.float32, dev, ts)
+              for t in (dq_out, dk_out))
+    return based_rotary_bwd(dq_out, dk_out, dq, dk, freqs, pos, layout, mscale, stream=ts)
+
+
+def gatedrec(x, g, h0=None, lengths=None, return_state: bool = False, for_grad: bool = False,
+             stream=None):
+    """y [B, L, D] of the gated recurrence; with return_state also the final
+    state [B, D], with for_grad also the saved states that gatedrec_grad needs."""
+    dev = _cuda(_device_of(x))
+    B, L, D = x.shape
+    ts = _torch_stream(stream, dev)
+    y = _new(x.shape, x.dtype, dev, ts)
+    h_last = _new((B, D), torch.float32, dev, ts) if return_state else None
+    chunks = (_new((B, -(-L // GATEDREC_CHUNK), D), torch.float32, dev, ts) if for_grad
+              else None)
+    based_gatedrec_fwd(x, g, y, h0, h_last, chunks, lengths, stream=ts)
+    out = (y,) + ((h_last,) if return_state else ()) + ((chunks,) if for_grad else ())
+    return out if len(out) > 1 else y
+
+
+def gatedrec_grad(x, g, dy, h_chunks, dh_last=None, lengths=None, stream=None):
+    """(dx, dg, dh0) in float32 given dy (and dh_last)."""
+    dev = _cuda(_device_of(x))
+    ts = _torch_stream(stream, dev)
+    dx, dg = (_new(x.shape, torch.float32, dev, ts) for _ in range(2))
+    dh0 = _new((x.shape[0], x.shape[2]), torch.float32, dev, ts)
+    return based_gatedrec_bwd(x, g, dy, h_chunks, dx, dg, dh_last, dh0, lengths, stream=ts)
+
+
+def gatedrec_step(x, g, h, stream=None):
+    """One token: y [B, D]; the state h [B, D] (float32) is updated in place."""
+    dev = _cuda(_device_of(x))
+    ts = _torch_stream(stream, dev)
+    return based_gatedrec_step(x, g, h, _new(x.shape, x.dtype, dev, ts), stream=ts)

@@ -9,6 +9,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <type_traits>
+
 #include "based.h"
 #include "common.cuh"
 #include "decode.cuh"
@@ -900,3 +902,5 @@ based_status_t based_get_device_error(based_stream_t stream) {
 }
 
 }  // extern "C"
+
+#include "layer_api.cuh"

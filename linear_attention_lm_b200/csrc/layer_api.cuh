@@ -1,0 +1,338 @@
+// layer_api.cuh -- entry points of the operators around a mixer: layer norm,
+// rotary positions, gated recurrence.  Part of based_api.cu's translation unit
+// (included at its end; uses its launch and checking helpers).
+#pragma once
+
+#include "gatedrec.cuh"
+#include "layernorm.cuh"
+#include "rotary.cuh"
+
+namespace {
+
+inline bool dtype_ok(based_dtype_t dt) { return dt == BASED_F32 || dt == BASED_BF16; }
+inline int dtype_bytes(based_dtype_t dt) { return dt == BASED_F32 ? 4 : 2; }
+inline long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+// Runs f(T{}, integral_constant<V>) for the type and the widest vector of at
+// most 16 bytes whose V divides n (row starts are then multiples of it).
+template <typename F>
+based_status_t for_vector(based_dtype_t dt, long long n, F f) {
+  using std::integral_constant;
+  if (dt == BASED_F32) {
+    if (n % 4 == 0) return f(float{}, integral_constant<int, 4>{});
+    if (n % 2 == 0) return f(float{}, integral_constant<int, 2>{});
+    return f(float{}, integral_constant<int, 1>{});
+  }
+  if (n % 8 == 0) return f(__nv_bfloat16{}, integral_constant<int, 8>{});
+  if (n % 4 == 0) return f(__nv_bfloat16{}, integral_constant<int, 4>{});
+  if (n % 2 == 0) return f(__nv_bfloat16{}, integral_constant<int, 2>{});
+  return f(__nv_bfloat16{}, integral_constant<int, 1>{});
+}
+
+// Warps of a row of D values at E values per thread: a power of two.
+inline int row_warps_for(int D, int E) {
+  int w = 1;
+  while ((long long)w * 32 * E < D) w *= 2;
+  return w;
+}
+
+template <typename T, int V, int E>
+based_status_t launch_layernorm_fwd(LnFwdParams p, cudaStream_t st) {
+  p.row_warps = row_warps_for(p.D, E);
+  const int tpr = p.row_warps * 32, threads = tpr > kLnThreads ? tpr : kLnThreads;
+  const long long blocks = ceil_div(p.rows, threads / tpr);
+  if (blocks > 0x7fffffffLL) return BASED_ERR_UNSUPPORTED;
+  if (!launch_dependent(layernorm_fwd_kernel<T, V, E>, dim3((unsigned)blocks), dim3(threads), 0, st,
+                        p))
+    return BASED_ERR_CUDA;
+  return launch_status();
+}
+
+struct LnBwdPlan {
+  int E, row_warps, threads, parts;
+};
+LnBwdPlan plan_layernorm_bwd(long long rows, int D) {
+  LnBwdPlan pl;
+  pl.E = D <= 256 ? 8 : 16;
+  pl.row_warps = row_warps_for(D, pl.E);
+  const int tpr = pl.row_warps * 32;
+  pl.threads = tpr > kLnThreads ? tpr : kLnThreads;
+  const long long want = ceil_div(rows, pl.threads / tpr);
+  const long long most = 2LL * device_sm_count();
+  pl.parts = (int)(want < most ? want : most);
+  return pl;
+}
+
+template <typename T, int V, int E>
+based_status_t launch_layernorm_bwd(LnBwdParams p, const LnBwdPlan& pl, float* dw, float* db,
+                                    cudaStream_t st) {
+  auto kern = layernorm_bwd_kernel<T, V, E>;
+  const size_t smem = pl.row_warps * 32 < pl.threads ? (size_t)p.D * 8 : 0;
+  if (!set_smem(kern, smem)) return BASED_ERR_CUDA;
+  p.row_warps = pl.row_warps;
+  if (pl.parts > 0 &&
+      !launch_dependent(kern, dim3((unsigned)pl.parts), dim3(pl.threads), smem, st, p))
+    return BASED_ERR_CUDA;
+  if (!launch_dependent(layernorm_parts_kernel, dim3((unsigned)ceil_div(2LL * p.D, 32)),
+                        dim3(32, 32), 0, st, (const float*)p.parts, pl.parts, p.D, dw, db))
+    return BASED_ERR_CUDA;
+  return launch_status();
+}
+
+based_status_t check_layernorm(long long rows, int D, based_dtype_t dt) {
+  if (rows < 0 || D <= 0 || !dtype_ok(dt)) return BASED_ERR_INVALID_ARG;
+  if (D > kLnMaxD || rows > (1LL << 47)) return BASED_ERR_UNSUPPORTED;
+  return BASED_OK;
+}
+
+based_status_t launch_rotary(RotaryParams p, int B, bool interleaved, based_dtype_t dt,
+                             cudaStream_t st) {
+  // 2V values per chunk: V has to divide half of the turned part and the head
+  const long long n = (p.rot / 2) % 8 == 0 && p.D % 8 == 0   ? 8
+                      : (p.rot / 2) % 4 == 0 && p.D % 4 == 0 ? 4
+                      : (p.rot / 2) % 2 == 0 && p.D % 2 == 0 ? 2
+                                                             : 1;
+  return for_vector(dt, n, [&](auto t, auto v) -> based_status_t {
+    using T = decltype(t);
+    constexpr int V = decltype(v)::value;
+    RotaryParams r = p;
+    r.rot_chunks = r.rot / (2 * V);
+    r.chunks = r.rot_chunks;
+    const bool in_place = (!r.H_q || r.q == r.q_out) && (!r.H_k || r.k == r.k_out);
+    if (!in_place) r.chunks += (int)ceil_div(r.D - r.rot, 2 * V);
+    r.items = (long long)B * r.L * r.chunks;
+    const long long blocks = ceil_div(r.items, kRotThreads);
+    if (blocks > 0x7fffffffLL) return BASED_ERR_UNSUPPORTED;
+    r.heads_per_cta = 8;
+    const dim3 grid((unsigned)blocks, (unsigned)ceil_div(r.H_q + r.H_k, r.heads_per_cta));
+    if (grid.y > 65535) return BASED_ERR_UNSUPPORTED;
+    const bool ok = interleaved ? launch_dependent(rotary_kernel<T, V, true>, grid,
+                                                   dim3(kRotThreads), 0, st, r)
+                                : launch_dependent(rotary_kernel<T, V, false>, grid,
+                                                   dim3(kRotThreads), 0, st, r);
+    if (!ok) return BASED_ERR_CUDA;
+    return launch_status();
+  });
+}
+
+based_status_t rotary_impl(const void* q, const void* k, void* q_out, void* k_out,
+                           const double* freqs, const long long* pos, long long pos0, int B,
+                           int H_q, int H_k, int L, int D, int rot_dim,
+                           based_rotary_layout_t layout, float mscale, bool inverse,
+                           based_dtype_t dt, based_stream_t stream) {
+  if (B < 0 || H_q < 0 || H_k < 0 || L < 0 || D <= 0 || rot_dim <= 0 || rot_dim > D ||
+      rot_dim % 2 != 0 || !dtype_ok(dt) || !isfinite(mscale))
+    return BASED_ERR_INVALID_ARG;
+  if (layout != BASED_ROTARY_HALF && layout != BASED_ROTARY_INTERLEAVED)
+    return BASED_ERR_INVALID_ARG;
+  if (!pos && pos0 < 0) return BASED_ERR_INVALID_ARG;
+  if (!pos && pos0 > (1LL << 31) - L) return BASED_ERR_UNSUPPORTED;
+  const bool no_q = (long long)B * H_q * L == 0, no_k = (long long)B * H_k * L == 0;
+  based_status_t s;
+  if ((s = check_tensor(q, no_q)) != BASED_OK) return s;
+  if ((s = check_tensor(q_out, no_q)) != BASED_OK) return s;
+  if ((s = check_tensor(k, no_k)) != BASED_OK) return s;
+  if ((s = check_tensor(k_out, no_k)) != BASED_OK) return s;
+  if (no_q && no_k) return BASED_OK;
+  if (!freqs || (reinterpret_cast<uintptr_t>(freqs) & 7u) ||
+      (reinterpret_cast<uintptr_t>(pos) & 7u))
+    return BASED_ERR_INVALID_ARG;
+  RotaryParams p{};
+  p.q = q; p.k = k; p.q_out = q_out; p.k_out = k_out;
+  p.freqs = freqs; p.pos_arr = pos; p.pos0 = pos0;
+  p.L = L; p.D = D; p.rot = rot_dim; p.H_q = H_q; p.H_k = H_k;
+  p.mscale = mscale; p.sign = inverse ? -1.0f : 1.0f;
+  return launch_rotary(p, B, layout == BASED_ROTARY_INTERLEAVED, dt,
+                       static_cast<cudaStream_t>(stream));
+}
+
+based_status_t check_gatedrec(const void* x, const void* g, const void* y, const void* lengths,
+                              int B, int L, int D, based_dtype_t dt) {
+  if (B < 0 || L < 0 || D <= 0 || !dtype_ok(dt)) return BASED_ERR_INVALID_ARG;
+  const bool empty = (long long)B * L == 0;
+  based_status_t s;
+  for (const void* t : {x, g, y})
+    if ((s = check_tensor(t, empty)) != BASED_OK) return s;
+  if (reinterpret_cast<uintptr_t>(lengths) & 7u) return BASED_ERR_INVALID_ARG;
+  if ((long long)B * ceil_div(D, 32) > 0x7fffffffLL) return BASED_ERR_UNSUPPORTED;
+  return BASED_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+based_status_t based_layernorm_fwd(const void* x, const void* residual, const float* weight,
+                                   const float* bias, void* y, void* resid_out, float* mean,
+                                   float* rstd, long long rows, int D, based_dtype_t dt, float eps,
+                                   based_stream_t stream) {
+  based_status_t s = check_layernorm(rows, D, dt);
+  if (s != BASED_OK) return s;
+  if (!(eps > 0.0f) || !isfinite(eps)) return BASED_ERR_INVALID_ARG;
+  if ((residual == nullptr) != (resid_out == nullptr) && rows > 0) return BASED_ERR_INVALID_ARG;
+  for (const void* t : {x, static_cast<const void*>(y), static_cast<const void*>(weight)})
+    if ((s = check_tensor(t, rows == 0)) != BASED_OK) return s;
+  for (const void* t : {residual, static_cast<const void*>(bias),
+                        static_cast<const void*>(resid_out), static_cast<const void*>(mean),
+                        static_cast<const void*>(rstd)})
+    if (!aligned16(t)) return BASED_ERR_INVALID_ARG;
+  if (rows == 0) return BASED_OK;
+  LnFwdParams p{};
+  p.x = x; p.residual = residual; p.w = weight; p.b = bias; p.y = y; p.resid_out = resid_out;
+  p.mean = mean; p.rstd = rstd; p.rows = rows; p.D = D; p.eps = eps;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return for_vector(dt, D, [&](auto t, auto v) {
+    using T = decltype(t);
+    constexpr int V = decltype(v)::value;
+    return D <= 256 ? launch_layernorm_fwd<T, V, 8>(p, st) : launch_layernorm_fwd<T, V, 32>(p, st);
+  });
+}
+
+size_t based_layernorm_bwd_workspace_bytes(long long rows, int D) {
+  if (check_layernorm(rows, D, BASED_F32) != BASED_OK) return (size_t)-1;
+  return (size_t)plan_layernorm_bwd(rows, D).parts * 2 * (size_t)D * sizeof(float);
+}
+
+based_status_t based_layernorm_bwd(const void* dy, const void* x, const float* weight,
+                                   const float* mean, const float* rstd, const float* dresid,
+                                   float* dx, float* dweight, float* dbias, long long rows, int D,
+                                   based_dtype_t dt, void* workspace, size_t workspace_bytes,
+                                   based_stream_t stream) {
+  based_status_t s = check_layernorm(rows, D, dt);
+  if (s != BASED_OK) return s;
+  for (const void* t : {dy, x, static_cast<const void*>(weight), static_cast<const void*>(mean),
+                        static_cast<const void*>(rstd), static_cast<const void*>(dx)})
+    if ((s = check_tensor(t, rows == 0)) != BASED_OK) return s;
+  if (!dweight || !aligned16(dweight) || !aligned16(dbias) || !aligned16(dresid))
+    return BASED_ERR_INVALID_ARG;
+  const LnBwdPlan pl = plan_layernorm_bwd(rows, D);
+  if (pl.parts > 0 &&
+      (!workspace || workspace_bytes < (size_t)pl.parts * 2 * (size_t)D * sizeof(float)))
+    return BASED_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return BASED_ERR_INVALID_ARG;
+  LnBwdParams p{};
+  p.dy = dy; p.x = x; p.w = weight; p.mean = mean; p.rstd = rstd; p.dresid = dresid;
+  p.dx = dx; p.parts = static_cast<float*>(workspace); p.rows = rows; p.D = D;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return for_vector(dt, D, [&](auto t, auto v) {
+    using T = decltype(t);
+    constexpr int V = decltype(v)::value;
+    return pl.E == 8 ? launch_layernorm_bwd<T, V, 8>(p, pl, dweight, dbias, st)
+                     : launch_layernorm_bwd<T, V, 16>(p, pl, dweight, dbias, st);
+  });
+}
+
+based_status_t based_rotary_freqs(double* freqs, int rot_dim, double base,
+                                  based_rotary_scaling_t scaling, double factor,
+                                  long long original_len, double low_turns, double high_turns) {
+  if (!freqs || rot_dim <= 0 || rot_dim % 2 != 0 || !(base > 0.0) || !isfinite(base))
+    return BASED_ERR_INVALID_ARG;
+  if (scaling != BASED_ROTARY_NONE && scaling != BASED_ROTARY_LINEAR &&
+      scaling != BASED_ROTARY_BY_PARTS)
+    return BASED_ERR_INVALID_ARG;
+  if (scaling != BASED_ROTARY_NONE && (!(factor >= 1.0) || !isfinite(factor)))
+    return BASED_ERR_INVALID_ARG;
+  if (scaling == BASED_ROTARY_BY_PARTS &&
+      (original_len < 1 || !(high_turns > low_turns) || !isfinite(high_turns) ||
+       !isfinite(low_turns)))
+    return BASED_ERR_INVALID_ARG;
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double f = pow(base, -2.0 * i / rot_dim) / (2.0 * M_PI);
+    if (scaling == BASED_ROTARY_LINEAR) f /= factor;
+    if (scaling == BASED_ROTARY_BY_PARTS) {
+      const double turns = f * (double)original_len;
+      double keep = (turns - low_turns) / (high_turns - low_turns);
+      keep = keep < 0.0 ? 0.0 : (keep > 1.0 ? 1.0 : keep);
+      f *= keep + (1.0 - keep) / factor;
+    }
+    freqs[i] = f;
+  }
+  return BASED_OK;
+}
+
+based_status_t based_rotary_fwd(const void* q, const void* k, void* q_out, void* k_out,
+                                const double* freqs, const long long* pos, long long pos0, int B,
+                                int H_q, int H_k, int L, int D, int rot_dim,
+                                based_rotary_layout_t layout, float mscale, based_dtype_t dt,
+                                based_stream_t stream) {
+  return rotary_impl(q, k, q_out, k_out, freqs, pos, pos0, B, H_q, H_k, L, D, rot_dim, layout,
+                     mscale, false, dt, stream);
+}
+
+based_status_t based_rotary_bwd(const float* dq_out, const float* dk_out, float* dq, float* dk,
+                                const double* freqs, const long long* pos, long long pos0, int B,
+                                int H_q, int H_k, int L, int D, int rot_dim,
+                                based_rotary_layout_t layout, float mscale,
+                                based_stream_t stream) {
+  return rotary_impl(dq_out, dk_out, dq, dk, freqs, pos, pos0, B, H_q, H_k, L, D, rot_dim, layout,
+                     mscale, true, BASED_F32, stream);
+}
+
+based_status_t based_gatedrec_fwd(const void* x, const void* g, void* y, const float* h0,
+                                  float* h_last, float* h_chunks, const long long* lengths, int B,
+                                  int L, int D, based_dtype_t dt, based_stream_t stream) {
+  based_status_t s = check_gatedrec(x, g, y, lengths, B, L, D, dt);
+  if (s != BASED_OK) return s;
+  if (!aligned16(h0) || !aligned16(h_last) || !aligned16(h_chunks)) return BASED_ERR_INVALID_ARG;
+  if (B == 0 || (L == 0 && !h_last)) return BASED_OK;
+  GrFwdParams p{};
+  p.x = x; p.g = g; p.y = y; p.h0 = h0; p.h_last = h_last; p.h_chunks = h_chunks;
+  p.lengths = lengths; p.B = B; p.L = L; p.D = D;
+  const dim3 grid((unsigned)((long long)B * ceil_div(D, 128)));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool ok = dt == BASED_F32
+                      ? launch_dependent(gatedrec_fwd_kernel<float>, grid, dim3(128), 0, st, p)
+                      : launch_dependent(gatedrec_fwd_kernel<__nv_bfloat16>, grid, dim3(128), 0,
+                                         st, p);
+  if (!ok) return BASED_ERR_CUDA;
+  return launch_status();
+}
+
+based_status_t based_gatedrec_bwd(const void* x, const void* g, const void* dy,
+                                  const float* h_chunks, const float* dh_last, float* dx, float* dg,
+                                  float* dh0, const long long* lengths, int B, int L, int D,
+                                  based_dtype_t dt, based_stream_t stream) {
+  based_status_t s = check_gatedrec(x, g, dy, lengths, B, L, D, dt);
+  if (s != BASED_OK) return s;
+  const bool empty = (long long)B * L == 0;
+  for (const void* t : {static_cast<const void*>(h_chunks), static_cast<const void*>(dx),
+                        static_cast<const void*>(dg)})
+    if ((s = check_tensor(t, empty)) != BASED_OK) return s;
+  if (!aligned16(dh_last) || !aligned16(dh0)) return BASED_ERR_INVALID_ARG;
+  if (B == 0 || (L == 0 && !dh0)) return BASED_OK;
+  GrBwdParams p{};
+  p.x = x; p.g = g; p.dy = dy; p.h_chunks = h_chunks; p.dh_last = dh_last;
+  p.dx = dx; p.dg = dg; p.dh0 = dh0; p.lengths = lengths; p.B = B; p.L = L; p.D = D;
+  const dim3 grid((unsigned)((long long)B * ceil_div(D, 64)));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool ok = dt == BASED_F32
+                      ? launch_dependent(gatedrec_bwd_kernel<float>, grid, dim3(64), 0, st, p)
+                      : launch_dependent(gatedrec_bwd_kernel<__nv_bfloat16>, grid, dim3(64), 0, st,
+                                         p);
+  if (!ok) return BASED_ERR_CUDA;
+  return launch_status();
+}
+
+based_status_t based_gatedrec_step(const void* x, const void* g, float* h, void* y, int B, int D,
+                                   based_dtype_t dt, based_stream_t stream) {
+  if (B < 0 || D <= 0 || !dtype_ok(dt)) return BASED_ERR_INVALID_ARG;
+  based_status_t s;
+  for (const void* t : {x, g, static_cast<const void*>(h), static_cast<const void*>(y)})
+    if ((s = check_tensor(t, B == 0)) != BASED_OK) return s;
+  if (B == 0) return BASED_OK;
+  const long long n = (long long)B * D;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return for_vector(dt, n, [&](auto t, auto v) -> based_status_t {
+    using T = decltype(t);
+    constexpr int V = decltype(v)::value;
+    const long long blocks = ceil_div(n, 128LL * V);
+    if (blocks > 0x7fffffffLL) return BASED_ERR_UNSUPPORTED;
+    if (!launch_dependent(gatedrec_step_kernel<T, V>, dim3((unsigned)blocks), dim3(128), 0, st,
+                          static_cast<const T*>(x), static_cast<const T*>(g), h,
+                          static_cast<T*>(y), n))
+      return BASED_ERR_CUDA;
+    return launch_status();
+  });
+}
+
+}  // extern "C"
