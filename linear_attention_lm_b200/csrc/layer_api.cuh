@@ -154,8 +154,51 @@ based_status_t check_gatedrec(const void* x, const void* g, const void* y, const
   for (const void* t : {x, g, y})
     if ((s = check_tensor(t, empty)) != BASED_OK) return s;
   if (reinterpret_cast<uintptr_t>(lengths) & 7u) return BASED_ERR_INVALID_ARG;
-  if ((long long)B * ceil_div(D, 32) > 0x7fffffffLL) return BASED_ERR_UNSUPPORTED;
+  if ((long long)B * ceil_div(D, 32) > 0x7fffffffLL || L > 0x7fff0000) return BASED_ERR_UNSUPPORTED;
   return BASED_OK;
+}
+
+// Runs f(T{}, integral_constant<V>) with the channels per lane.
+template <typename F>
+based_status_t for_channels(based_dtype_t dt, int D, F f) {
+  using std::integral_constant;
+  if (dt == BASED_F32)
+    return D % 2 == 0 ? f(float{}, integral_constant<int, 2>{})
+                      : f(float{}, integral_constant<int, 1>{});
+  return D % 2 == 0 ? f(__nv_bfloat16{}, integral_constant<int, 2>{})
+                    : f(__nv_bfloat16{}, integral_constant<int, 1>{});
+}
+
+// Launches kern on B * n_blk clusters of N CTAs, as a dependent launch.
+template <typename P>
+bool launch_gatedrec(void (*kern)(P), const P& p, long long clusters, cudaStream_t st) {
+  if (p.N > 8 &&
+      cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    return false;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)p.N;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)(clusters * p.N));
+  cfg.blockDim = dim3(kGrThreads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.N > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess;
+}
+
+// CTAs per cluster: as many as fit on the GPU at once at two CTAs per SM, and no
+// more than there are tiles.
+inline int gatedrec_cluster(long long clusters, int L, int tile) {
+  int N = 1;
+  while (2 * N <= kGrMaxCluster && clusters * 2 * N <= 2LL * device_sm_count() &&
+         (long long)N * tile < L)
+    N *= 2;
+  return N;
 }
 
 }  // namespace
@@ -277,15 +320,17 @@ based_status_t based_gatedrec_fwd(const void* x, const void* g, void* y, const f
   if (B == 0 || (L == 0 && !h_last)) return BASED_OK;
   GrFwdParams p{};
   p.x = x; p.g = g; p.y = y; p.h0 = h0; p.h_last = h_last; p.h_chunks = h_chunks;
-  p.lengths = lengths; p.B = B; p.L = L; p.D = D;
-  const dim3 grid((unsigned)((long long)B * ceil_div(D, 128)));
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool ok = dt == BASED_F32
-                      ? launch_dependent(gatedrec_fwd_kernel<float>, grid, dim3(128), 0, st, p)
-                      : launch_dependent(gatedrec_fwd_kernel<__nv_bfloat16>, grid, dim3(128), 0,
-                                         st, p);
-  if (!ok) return BASED_ERR_CUDA;
-  return launch_status();
+  p.lengths = lengths; p.L = L; p.D = D;
+  return for_channels(dt, D, [&](auto t, auto v) -> based_status_t {
+    using T = decltype(t);
+    constexpr int V = decltype(v)::value;
+    p.n_blk = (int)ceil_div(D, 32 * V);
+    const long long clusters = (long long)B * p.n_blk;
+    p.N = gatedrec_cluster(clusters, L, GrShape<T, V>::kTile);
+    if (!launch_gatedrec(gatedrec_fwd_kernel<T, V>, p, clusters, static_cast<cudaStream_t>(stream)))
+      return BASED_ERR_CUDA;
+    return launch_status();
+  });
 }
 
 based_status_t based_gatedrec_bwd(const void* x, const void* g, const void* dy,
@@ -302,15 +347,17 @@ based_status_t based_gatedrec_bwd(const void* x, const void* g, const void* dy,
   if (B == 0 || (L == 0 && !dh0)) return BASED_OK;
   GrBwdParams p{};
   p.x = x; p.g = g; p.dy = dy; p.h_chunks = h_chunks; p.dh_last = dh_last;
-  p.dx = dx; p.dg = dg; p.dh0 = dh0; p.lengths = lengths; p.B = B; p.L = L; p.D = D;
-  const dim3 grid((unsigned)((long long)B * ceil_div(D, 64)));
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool ok = dt == BASED_F32
-                      ? launch_dependent(gatedrec_bwd_kernel<float>, grid, dim3(64), 0, st, p)
-                      : launch_dependent(gatedrec_bwd_kernel<__nv_bfloat16>, grid, dim3(64), 0, st,
-                                         p);
-  if (!ok) return BASED_ERR_CUDA;
-  return launch_status();
+  p.dx = dx; p.dg = dg; p.dh0 = dh0; p.lengths = lengths; p.L = L; p.D = D;
+  return for_channels(dt, D, [&](auto t, auto v) -> based_status_t {
+    using T = decltype(t);
+    constexpr int V = decltype(v)::value;
+    p.n_blk = (int)ceil_div(D, 32 * V);
+    const long long clusters = (long long)B * p.n_blk;
+    p.N = gatedrec_cluster(clusters, L, kGrChunk);
+    if (!launch_gatedrec(gatedrec_bwd_kernel<T, V>, p, clusters, static_cast<cudaStream_t>(stream)))
+      return BASED_ERR_CUDA;
+    return launch_status();
+  });
 }
 
 based_status_t based_gatedrec_step(const void* x, const void* g, float* h, void* y, int B, int D,
