@@ -17,150 +17,173 @@ constexpr int kGrChunk = 64;  // tokens between two saved states
 
 // a = sigmoid(g) and n = 1 - a.  The smaller of the two is formed with its full
 // relative precision, t = e / (1 + e) with e = exp(-|g|), and the other is its
-// complement to 1, so that a slow decay (1 - a << 1) keeps its rate.
+// complement to 1, so that a slow decay (1 - a << 1) keeps its rate.  The
+// reciprocal is the hardware's (about 2^-23 off; its argument is in [1, 2]).
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 struct Gate {
   float a, n;
 };
 __device__ __forceinline__ Gate gate_of(float g) {
   const float e = ex2_approx(-1.4426950408889634f * fabsf(g));
-  const float t = __fdividef(e, 1.0f + e);
+  const float t = e * rcp_approx(1.0f + e);
   const float u = 1.0f - t;
   return g >= 0.0f ? Gate{u, t} : Gate{t, u};
 }
+struct Gate2 {
+  F2 a, n;
+};
+__device__ __forceinline__ Gate2 gate_of(F2 g2) {
+  const float2 g = f2_get(g2);
+  const float ex = ex2_approx(-1.4426950408889634f * fabsf(g.x));
+  const float ey = ex2_approx(-1.4426950408889634f * fabsf(g.y));
+  const F2 e = f2(ex, ey), one = f2(1.0f, 1.0f);
+  const float2 d = f2_get(e + one);
+  const F2 t2 = e * f2(rcp_approx(d.x), rcp_approx(d.y));
+  const float2 t = f2_get(t2), u = f2_get(f2_fma(t2, f2(-1.0f, -1.0f), one));
+  const bool px = g.x >= 0.0f, py = g.y >= 0.0f;
+  return Gate2{f2(px ? u.x : t.x, py ? u.y : t.y), f2(px ? t.x : u.x, py ? t.y : u.y)};
+}
 
-// How the sequence is cut: lanes own V neighbouring channels, a warp S tokens, a
-// CTA kGrWarps warps, one after another (a tile of T = 8 S tokens), and a cluster
-// of N CTAs walks the sequence N tiles at a time.  A tile is read once, into
-// registers.  Each warp forms its tokens' map h -> A h + H (A the product of its
-// gates, H its end state from zero), the maps of the CTA's warps meet in shared
-// memory and those of the cluster's CTAs in every CTA's shared memory (one
-// cluster barrier per N tiles); then every warp knows the state that enters its
-// tokens and runs them again from its registers.  The next tile's loads are
-// issued before the barriers, so memory stays busy across them.
+// How the sequence is cut: a CTA takes 64 channels, two per lane; a warp S tokens,
+// a CTA kGrWarps warps, one after another (a tile of kGrWarps S tokens), and a
+// cluster of N CTAs walks the sequence N tiles at a time.  Each warp forms its
+// tokens' map h -> A h + H (A the product of its gates, H its end state from
+// zero), the maps of the CTA's warps meet in shared memory and those of the
+// cluster's CTAs in every CTA's shared memory (one cluster barrier per N tiles);
+// then every warp knows the state that enters its tokens and runs them again
+// from its registers.  Inputs are read once: each warp copies its own tokens of
+// the next tiles into a ring of kGrStages slots (cp.async), so loads run ahead of
+// the barriers and hold no registers.
 constexpr int kGrWarps = 8;
 constexpr int kGrThreads = 32 * kGrWarps;
-constexpr int kGrMaxCluster = 16;
+constexpr int kGrCols = 64;
+constexpr int kGrStages = 3;
+constexpr int kGrMaxCluster = 8;
 
-template <typename T, int V>
-struct GrShape {
-  // about 128 bytes of x and g in flight per thread; T a multiple of kGrChunk
-  static constexpr int S = V * sizeof(T) >= 8 ? 8 : 16;
-  static constexpr int kTile = S * kGrWarps;
-};
-
-// V channels' maps as one shared-memory vector per lane
-template <int V>
+// A map of two channels per lane in shared memory: A, H of the one, of the other
 struct GrMap {
-  float A[V], H[V];
+  F2 A, H;
 };
-template <int V>
-__device__ __forceinline__ void map_store(float* p, const GrMap<V>& m) {
-  if constexpr (V == 1) {
-    *reinterpret_cast<float2*>(p) = make_float2(m.A[0], m.H[0]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; i += 2)
-      *reinterpret_cast<float4*>(p + 2 * i) = make_float4(m.A[i], m.H[i], m.A[i + 1], m.H[i + 1]);
-  }
+__device__ __forceinline__ GrMap map_one() { return GrMap{f2(1.0f, 1.0f), f2(0.0f, 0.0f)}; }
+__device__ __forceinline__ void map_store(ulonglong2* p, const GrMap& m) {
+  *p = make_ulonglong2(m.A.v, m.H.v);
 }
-template <int V>
-__device__ __forceinline__ GrMap<V> map_load(const float* p) {
-  GrMap<V> m;
-  if constexpr (V == 1) {
-    const float2 v = *reinterpret_cast<const float2*>(p);
-    m.A[0] = v.x; m.H[0] = v.y;
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; i += 2) {
-      const float4 v = *reinterpret_cast<const float4*>(p + 2 * i);
-      m.A[i] = v.x; m.H[i] = v.y; m.A[i + 1] = v.z; m.H[i + 1] = v.w;
-    }
-  }
-  return m;
+__device__ __forceinline__ GrMap map_load(const ulonglong2* p) {
+  const ulonglong2 v = *p;
+  return GrMap{F2{v.x}, F2{v.y}};
 }
-// into CTA `rank` of the cluster, at the place that p has in this CTA
-template <int V>
-__device__ __forceinline__ void map_store_peer(float* p, uint32_t rank, const GrMap<V>& m) {
-  const uint32_t at = umma::cluster_addr(p, rank);
-#pragma unroll
-  for (int i = 0; i < V; ++i)
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at + 8 * i), "f"(m.A[i]),
-                 "f"(m.H[i])
-                 : "memory");
+__device__ __forceinline__ void map_then(GrMap& m, const GrMap& next) {
+  m.H = f2_fma(next.A, m.H, next.H);
+  m.A = m.A * next.A;
 }
-// m, then next
-template <int V>
-__device__ __forceinline__ void map_then(GrMap<V>& m, const GrMap<V>& next) {
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    m.H[v] = fmaf(next.A[v], m.H[v], next.H[v]);
-    m.A[v] *= next.A[v];
-  }
-}
-template <int V>
-__device__ __forceinline__ void map_apply(float (&h)[V], const GrMap<V>& m) {
-#pragma unroll
-  for (int v = 0; v < V; ++v) h[v] = fmaf(m.A[v], h[v], m.H[v]);
-}
+__device__ __forceinline__ void map_apply(F2& h, const GrMap& m) { h = f2_fma(m.A, h, m.H); }
 
-// Maps of a CTA's warps and of a cluster's CTAs, two sets in turn.  A set is
-// written again two rounds later, behind a barrier that every reader of the
-// first round has passed.
-template <int V>
+// Maps of a CTA's warps and of a cluster's CTAs, two sets in turn.  The CTAs send
+// each other their maps with stores that complete on the receiver's barrier of
+// the set (a cluster barrier would also wait for the outputs' stores to global
+// memory: 29.1 against 27.0 us for 8 x 2048 x 1024 bf16).  A set is written again two rounds later: a CTA
+// sends in round k + 2 when it has received round k + 1 of every CTA, and each
+// sent that when all its warps had read the set of round k.
 struct GrShared {
-  float warp[2][kGrWarps][32 * 2 * V];
-  float cta[2][kGrMaxCluster][32 * 2 * V];
+  ulonglong2 warp[2][kGrWarps][32];
+  ulonglong2 cta[2][kGrMaxCluster][32];
+  uint64_t bar[2];
+  uint64_t pad[6];
 };
+__device__ __forceinline__ uint32_t gr_round_bytes(int N) { return (uint32_t)N * 32 * 16; }
 
-// One round: every warp of the cluster gives its map `mine`, in the order of the
-// scan (order index of this warp w, of this CTA r: position in the scan, not
-// rank).  h: the state that enters the round; on return the state that leaves
-// it, and `enter` the one that enters this warp's tokens.  `to(r)` is the rank
-// of the CTA at position r.
-template <int V, typename Rank>
-__device__ __forceinline__ void gr_round(GrShared<V>& sh, int buf, int w, int r, int N, int lane,
-                                         const GrMap<V>& mine, float (&h)[V], float (&enter)[V],
-                                         Rank to) {
-  map_store<V>(&sh.warp[buf][w][lane * 2 * V], mine);
-  __syncthreads();
-  GrMap<V> before, all;
+// Before the first round; also: every CTA of the cluster has started.
+__device__ __forceinline__ void gr_cluster_begin(GrShared& sh, int N) {
+  if (N == 1) return;
+  if (threadIdx.x == 0) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    all.A[v] = before.A[v] = 1.0f;
-    all.H[v] = before.H[v] = 0.0f;
+    for (int i = 0; i < 2; ++i) umma::mbar_init(&sh.bar[i], 1);
+    umma::fence_mbar_init();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) umma::mbar_arrive_expect_tx(&sh.bar[i], gr_round_bytes(N));
   }
+  __syncwarp();
+  umma::cluster_sync();
+}
+
+// After the last round: no CTA leaves before the others' sends to it (or their
+// giving up), and every thread of the cluster has read h0.
+__device__ __forceinline__ void gr_cluster_end(int N, bool ok) {
+  if (!ok) record_device_error(BASED_ERR_TIMEOUT);
+  __syncwarp();
+  if (N > 1) umma::cluster_sync();
+  else __syncthreads();
+}
+
+// One round k: every warp of the cluster gives its map `mine`; w and r are the
+// positions of the warp in its CTA and of the CTA in its cluster in the order of
+// the scan, to(r) the rank of the CTA at position r.  h: the state that enters
+// the round; on return the state that leaves it, and `enter` the one that enters
+// this warp's tokens.  False: a wait was given up (and every later one is).
+template <typename Rank>
+__device__ __forceinline__ bool gr_round(GrShared& sh, int k, int w, int r, int N, int lane,
+                                         const GrMap& mine, F2& h, F2& enter, bool ok, Rank to) {
+  const int buf = k & 1;
+  map_store(&sh.warp[buf][w][lane], mine);
+  __syncthreads();
+  GrMap before = map_one(), all = map_one();
 #pragma unroll
   for (int i = 0; i < kGrWarps; ++i) {
     if (i == w) before = all;
-    map_then<V>(all, map_load<V>(&sh.warp[buf][i][lane * 2 * V]));
+    map_then(all, map_load(&sh.warp[buf][i][lane]));
   }
   if (N > 1) {
-    for (int k = w; k < N; k += kGrWarps)
-      map_store_peer<V>(&sh.cta[buf][r][lane * 2 * V], (uint32_t)to(k), all);
-    umma::cluster_sync();
-    for (int k = 0; k < N; ++k) {
-      if (k == r) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) enter[v] = h[v];
-      }
-      map_apply<V>(h, map_load<V>(&sh.cta[buf][k][lane * 2 * V]));
+    if (w < N)
+      umma::st_async_16(umma::cluster_addr(&sh.cta[buf][r][lane], (uint32_t)to(w)), all.A.v,
+                        all.H.v, umma::cluster_addr(&sh.bar[buf], (uint32_t)to(w)));
+    if (ok) ok = umma::mbar_wait_cluster_inline(&sh.bar[buf], (k >> 1) & 1);
+    if (threadIdx.x == 0 && ok) umma::mbar_arrive_expect_tx(&sh.bar[buf], gr_round_bytes(N));  // k + 2
+    for (int i = 0; i < N; ++i) {
+      if (i == r) enter = h;
+      map_apply(h, map_load(&sh.cta[buf][i][lane]));
     }
   } else {
-#pragma unroll
-    for (int v = 0; v < V; ++v) enter[v] = h[v];
-    map_apply<V>(h, all);
+    enter = h;
+    map_apply(h, all);
   }
-  map_apply<V>(enter, before);
+  map_apply(enter, before);
+  return ok;
 }
+static_assert(kGrMaxCluster <= kGrWarps, "warp i sends to the CTA at position i");
 
-struct GrFwdParams {
-  const void *x, *g;
-  void* y;
-  const float* h0;
-  float *h_last, *h_chunks;
-  const long long* lengths;
-  int L, D, n_blk, N;  // n_blk: channel blocks of a sequence; N: CTAs per cluster
-};
+// Copies S tokens x 64 channels of a sequence (row length D, from token t0 on) into
+// `slot` [S][64]; tokens from `end` on and channels from `cols` on become zero.
+// CW bytes at a time: the widest size that divides a row.  Rows of an odd number
+// of bf16 have no asynchronous copy and are copied through registers.
+template <typename T, int S, int CW>
+__device__ __forceinline__ void gr_fetch(T* slot, const T* src, int D, int t0, int end, int cols,
+                                         int lane) {
+  constexpr int E = CW / (int)sizeof(T), RC = kGrCols / E;  // elements per copy, copies per row
+  auto copy = [](T* to, const T* from, bool in) {
+    if constexpr (CW == 16) umma::cp_async16(to, from, in);
+    else if constexpr (CW >= 4) umma::cp_async_small<CW>(to, from, in);
+    else *to = in ? *from : from_f32<T>(0.0f);
+  };
+  if (CW == 16 && t0 + S <= end && cols == kGrCols) {
+    const int row = lane / RC, col = lane % RC * E;
+    const T* from = src + ((size_t)(t0 + row) * D + col);
+    T* to = slot + row * kGrCols + col;
+#pragma unroll
+    for (int i = 0; i < S * RC / 32; ++i, from += (size_t)(32 / RC) * D)
+      copy(to + i * (32 / RC) * kGrCols, from, true);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < S * RC / 32; ++i) {
+    const int row = (i * 32 + lane) / RC, col = (i * 32 + lane) % RC * E;
+    const bool in = t0 + row < end && col < cols;
+    copy(slot + row * kGrCols + col, src + (in ? (size_t)(t0 + row) * D + col : 0), in);
+  }
+}
 
 // Length of sequence b; -1 (and a recorded error) if the array's entry is not in [0, L].
 __device__ __forceinline__ int gr_length(const long long* lengths, int b, int L) {
@@ -173,87 +196,125 @@ __device__ __forceinline__ int gr_length(const long long* lengths, int b, int L)
   return (int)n;
 }
 
+// Two channels of an fp32 [.., D] row at p; kPair: rows start at even elements.
+template <bool kPair>
+__device__ __forceinline__ F2 gr_load(const float* p, bool two) {
+  if constexpr (kPair) return load_pair(p);
+  else return f2(p[0], two ? p[1] : 0.0f);
+}
+template <bool kPair, typename T>
+__device__ __forceinline__ void gr_store(T* p, F2 v, bool two) {
+  if constexpr (kPair) store_pair(p, v);
+  else store_ends(p, v, two);
+}
+
+struct GrFwdParams {
+  const void *x, *g;
+  void* y;
+  const float* h0;
+  float *h_last, *h_chunks;
+  const long long* lengths;
+  int L, D, n_blk, N;  // n_blk: channel blocks of a sequence; N: CTAs per cluster
+};
+
+template <typename T>
+struct GrFwdShape {
+  static constexpr int S = 32 / (int)sizeof(T);  // a ring slot of x and g: 4 KiB per warp
+  static constexpr int kTile = S * kGrWarps;
+  static constexpr int kSlot = 2 * S * kGrCols;  // elements
+  static constexpr size_t kSmem = sizeof(GrShared) + sizeof(T) * kGrWarps * kGrStages * kSlot;
+  static_assert(kGrChunk % S == 0 && kTile % kGrChunk == 0, "chunks start with a warp's tokens");
+};
+
 // The number of rounds goes by L alone, never by what memory holds: every thread
 // of a cluster reaches the same barriers.
-template <typename T, int V>
+template <typename T, int CW>
 __global__ void __launch_bounds__(kGrThreads, 2) gatedrec_fwd_kernel(const GrFwdParams p) {
-  constexpr int S = GrShape<T, V>::S, kTile = GrShape<T, V>::kTile;
-  __shared__ __align__(16) GrShared<V> sh;
-  if (p.N > 1) umma::cluster_sync();  // every CTA has started before its shared memory is written
+  using Shape = GrFwdShape<T>;
+  constexpr int S = Shape::S, kTile = Shape::kTile;
+  constexpr bool kPair = CW > (int)sizeof(T);
+  extern __shared__ __align__(16) unsigned char gr_smem[];
+  GrShared& sh = *reinterpret_cast<GrShared*>(gr_smem);
+  gr_cluster_begin(sh, p.N);
   umma::grid_dep_wait();
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  T* ring = reinterpret_cast<T*>(gr_smem + sizeof(GrShared)) + w * kGrStages * Shape::kSlot;
   const int rank = blockIdx.x % p.N, cid = blockIdx.x / p.N;
-  const int b = cid / p.n_blk, c = (cid % p.n_blk * 32 + lane) * V;
-  const int len = gr_length(p.lengths, b, p.L);
-  const bool live = c < p.D && len >= 0;
-  const int end = live ? len : 0;  // tokens this lane reads
-  const size_t base = (size_t)b * p.L * p.D + c;
+  const int b = cid / p.n_blk, c0 = cid % p.n_blk * kGrCols, c = c0 + 2 * lane;
+  const int len = gr_length(p.lengths, b, p.L), end = max(len, 0);
+  const bool live = c < p.D && len >= 0, two = c + 1 < p.D;
+  const int cols = min(p.D - c0, kGrCols);
+  const T* x = static_cast<const T*>(p.x) + (size_t)b * p.L * p.D + c0;
+  const T* g = static_cast<const T*>(p.g) + (size_t)b * p.L * p.D + c0;
+  T* y = static_cast<T*>(p.y) + (size_t)b * p.L * p.D + c;
   const int n_chunks = (p.L + kGrChunk - 1) / kGrChunk;
 
-  float h[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) h[v] = 0.0f;
-  if (live && p.h0) load_f32<V>(p.h0 + (size_t)b * p.D + c, h);
+  F2 h = f2(0.0f, 0.0f);
+  if (live && p.h0) h = gr_load<kPair>(p.h0 + (size_t)b * p.D + c, two);
 
-  Pack<T, V> xr[S], gr[S];
-  auto fetch = [&](int t0) {
-    const T* x = static_cast<const T*>(p.x) + base + (size_t)t0 * p.D;
-    const T* g = static_cast<const T*>(p.g) + base + (size_t)t0 * p.D;
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-      if (t0 + s < end) {
-        xr[s].load(x + (size_t)s * p.D);
-        gr[s].load(g + (size_t)s * p.D);
-      }
-    }
-  };
-  int t0 = rank * kTile + w * S;
-  fetch(t0);
   const int rounds = (p.L + p.N * kTile - 1) / (p.N * kTile);
-  for (int k = 0; k < rounds; ++k, t0 += p.N * kTile) {
-    float a[S][V], u[S][V];  // h -> a h + u; the identity past the end
-    GrMap<V> m;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      m.A[v] = 1.0f;
-      m.H[v] = 0.0f;
+  auto fetch = [&](int k) {
+    if (k < rounds) {
+      T* slot = ring + k % kGrStages * Shape::kSlot;
+      const int t0 = (k * p.N + rank) * kTile + w * S;
+      gr_fetch<T, S, CW>(slot, x, p.D, t0, end, cols, lane);
+      gr_fetch<T, S, CW>(slot + S * kGrCols, g, p.D, t0, end, cols, lane);
     }
+    umma::cp_async_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < kGrStages - 1; ++k) fetch(k);
+  bool ok = true;
+  for (int k = 0; k < rounds; ++k) {
+    const int t0 = (k * p.N + rank) * kTile + w * S;
+    umma::cp_async_wait<kGrStages - 2>();
+    __syncwarp();
+    fetch(k + kGrStages - 1);  // into the slot read in the round before
+    const T* xs = ring + k % kGrStages * Shape::kSlot + 2 * lane;
+    const T* gs = xs + S * kGrCols;
+    F2 a[S], u[S];  // h -> a h + u
+    GrMap m = map_one();
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      const bool in = t0 + s < end;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const Gate gt = gate_of(gr[s].get(v));
-        a[s][v] = in ? gt.a : 1.0f;
-        u[s][v] = in ? gt.n * xr[s].get(v) : 0.0f;
-        m.H[v] = fmaf(a[s][v], m.H[v], u[s][v]);
-        m.A[v] *= a[s][v];
-      }
+      const Gate2 gt = gate_of(load_pair(gs + s * kGrCols));
+      a[s] = gt.a;
+      u[s] = gt.n * load_pair(xs + s * kGrCols);
     }
-    if (k + 1 < rounds) fetch(t0 + p.N * kTile);
-    float e[V];
-    gr_round<V>(sh, k & 1, w, rank, p.N, lane, m, h, e, [](int r) { return r; });
-    if (live && p.h_chunks && t0 % kGrChunk == 0 && t0 < p.L) {
-      float o[V];
+    if (t0 + S > end) {  // past the end: the identity
 #pragma unroll
-      for (int v = 0; v < V; ++v) o[v] = t0 < end ? e[v] : 0.0f;
-      store_f32<V>(p.h_chunks + ((size_t)b * n_chunks + t0 / kGrChunk) * p.D + c, o);
+      for (int s = 0; s < S; ++s)
+        if (t0 + s >= end) {
+          a[s] = f2(1.0f, 1.0f);
+          u[s] = f2(0.0f, 0.0f);
+        }
     }
-    T* y = static_cast<T*>(p.y) + base + (size_t)t0 * p.D;
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      Pack<T, V> o;
+    for (int s = 0; s < S; ++s) map_then(m, GrMap{a[s], u[s]});
+    F2 e;
+    ok = gr_round(sh, k, w, rank, p.N, lane, m, h, e, ok, [](int r) { return r; });
+    if (live) {
+      if (p.h_chunks && t0 % kGrChunk == 0 && t0 < p.L)
+        gr_store<kPair>(p.h_chunks + ((size_t)b * n_chunks + t0 / kGrChunk) * p.D + c,
+                        t0 < end ? e : f2(0.0f, 0.0f), two);
+      T* out = y + (size_t)t0 * p.D;
+      if (t0 + S <= end) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        e[v] = fmaf(a[s][v], e[v], u[s][v]);
-        o.set(v, t0 + s < end ? e[v] : 0.0f);
+        for (int s = 0; s < S; ++s, out += p.D) {
+          e = f2_fma(a[s], e, u[s]);
+          gr_store<kPair>(out, e, two);
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < S; ++s, out += p.D) {
+          e = f2_fma(a[s], e, u[s]);
+          if (t0 + s < p.L) gr_store<kPair>(out, t0 + s < end ? e : f2(0.0f, 0.0f), two);
+        }
       }
-      if (live && t0 + s < p.L) o.store(y + (size_t)s * p.D);
     }
   }
+  gr_cluster_end(p.N, ok);
   if (p.h_last) {
-    __syncthreads();  // h_last may be h0: every warp has read it (other CTAs: the rounds' barriers)
-    if (live && rank == 0 && w == 0) store_f32<V>(p.h_last + (size_t)b * p.D + c, h);
+    if (live && rank == 0 && w == 0) gr_store<kPair>(p.h_last + (size_t)b * p.D + c, h, two);
   }
 }
 
@@ -265,124 +326,127 @@ struct GrBwdParams {
   int L, D, n_blk, N;
 };
 
-template <typename T, int V>
+template <typename T>
 struct GrBwdShape {
   // tiles of one chunk: the forward states of a tile start from its saved state
   static constexpr int S = kGrChunk / kGrWarps;
+  static constexpr int kSlot = 3 * S * kGrCols;
+  static constexpr size_t kShared = sizeof(GrShared) + sizeof(ulonglong2) * 2 * kGrWarps * 32;
+  static constexpr size_t kSmem = kShared + sizeof(T) * kGrWarps * kGrStages * kSlot;
 };
 
 // The same cut, walked from the end.  The state that enters a tile is the saved
 // one, so the forward maps only have to meet inside the CTA; the gradient's maps
 // l -> A l + Q go through the cluster.
-template <typename T, int V>
+template <typename T, int CW>
 __global__ void __launch_bounds__(kGrThreads, 2) gatedrec_bwd_kernel(const GrBwdParams p) {
-  constexpr int S = GrBwdShape<T, V>::S, kTile = S * kGrWarps;
-  static_assert(kTile == kGrChunk, "one saved state per tile");
-  __shared__ __align__(16) GrShared<V> sh;
-  __shared__ __align__(16) float fwd[2][kGrWarps][32 * 2 * V];
-  if (p.N > 1) umma::cluster_sync();
+  using Shape = GrBwdShape<T>;
+  constexpr int S = Shape::S, kTile = kGrChunk;
+  constexpr bool kPair = CW > (int)sizeof(T);
+  extern __shared__ __align__(16) unsigned char gr_smem[];
+  GrShared& sh = *reinterpret_cast<GrShared*>(gr_smem);
+  auto fwd = reinterpret_cast<ulonglong2(*)[kGrWarps][32]>(gr_smem + sizeof(GrShared));
+  gr_cluster_begin(sh, p.N);
   umma::grid_dep_wait();
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  T* ring = reinterpret_cast<T*>(gr_smem + Shape::kShared) + w * kGrStages * Shape::kSlot;
   const int rank = blockIdx.x % p.N, cid = blockIdx.x / p.N;
-  const int b = cid / p.n_blk, c = (cid % p.n_blk * 32 + lane) * V;
-  const int len = gr_length(p.lengths, b, p.L);
-  const bool live = c < p.D && len >= 0;
-  const int end = live ? len : 0;
-  const size_t base = (size_t)b * p.L * p.D + c;
+  const int b = cid / p.n_blk, c0 = cid % p.n_blk * kGrCols, c = c0 + 2 * lane;
+  const int len = gr_length(p.lengths, b, p.L), end = max(len, 0);
+  const bool live = c < p.D && len >= 0, two = c + 1 < p.D;
+  const int cols = min(p.D - c0, kGrCols);
+  const size_t seq = (size_t)b * p.L * p.D;
+  const T* x = static_cast<const T*>(p.x) + seq + c0;
+  const T* g = static_cast<const T*>(p.g) + seq + c0;
+  const T* dy = static_cast<const T*>(p.dy) + seq + c0;
   const int n_chunks = (p.L + kGrChunk - 1) / kGrChunk;
+  const F2 zero = f2(0.0f, 0.0f), minus = f2(-1.0f, -1.0f);
 
-  float l[V];  // a_{t+1} l_{t+1} at the end of the round
-#pragma unroll
-  for (int v = 0; v < V; ++v) l[v] = 0.0f;
-  if (live && p.dh_last) load_f32<V>(p.dh_last + (size_t)b * p.D + c, l);
+  F2 l = zero;  // a_{t+1} l_{t+1} at the end of the round
+  if (live && p.dh_last) l = gr_load<kPair>(p.dh_last + (size_t)b * p.D + c, two);
 
-  Pack<T, V> xr[S], gr[S], dr[S];
-  float hc[V];
-  auto fetch = [&](int t0) {
-    const size_t at = base + (size_t)t0 * p.D;
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-      if (t0 + s < end) {
-        xr[s].load(static_cast<const T*>(p.x) + at + (size_t)s * p.D);
-        gr[s].load(static_cast<const T*>(p.g) + at + (size_t)s * p.D);
-        dr[s].load(static_cast<const T*>(p.dy) + at + (size_t)s * p.D);
-      }
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) hc[v] = 0.0f;
-    if (t0 < end)
-      load_f32<V>(p.h_chunks + ((size_t)b * n_chunks + t0 / kGrChunk) * p.D + c, hc);
-  };
   const int rounds = (p.L + p.N * kTile - 1) / (p.N * kTile);
-  int t0 = (rounds - 1) * p.N * kTile + rank * kTile + w * S;
-  if (rounds > 0) fetch(t0);
-  for (int k = 0; k < rounds; ++k, t0 -= p.N * kTile) {
-    float a[S][V], n[S][V], x[S][V], d[S][V];
-    GrMap<V> f, q;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      f.A[v] = 1.0f;
-      f.H[v] = q.H[v] = 0.0f;
+  auto first = [&](int k) { return ((rounds - 1 - k) * p.N + rank) * kTile; };  // the tile's token
+  auto fetch = [&](int k) {
+    if (k < rounds) {
+      T* slot = ring + k % kGrStages * Shape::kSlot;
+      const int t0 = first(k) + w * S;
+      gr_fetch<T, S, CW>(slot, x, p.D, t0, end, cols, lane);
+      gr_fetch<T, S, CW>(slot + S * kGrCols, g, p.D, t0, end, cols, lane);
+      gr_fetch<T, S, CW>(slot + 2 * S * kGrCols, dy, p.D, t0, end, cols, lane);
     }
+    umma::cp_async_commit();
+  };
+  auto saved = [&](int k) {
+    if (k >= rounds || !live || first(k) >= end) return zero;
+    return gr_load<kPair>(p.h_chunks + ((size_t)b * n_chunks + first(k) / kGrChunk) * p.D + c, two);
+  };
+#pragma unroll
+  for (int k = 0; k < kGrStages - 1; ++k) fetch(k);
+  bool ok = true;
+  F2 next = saved(0);
+  for (int k = 0; k < rounds; ++k) {
+    const int t0 = first(k) + w * S;
+    F2 h = next;  // the state that enters the tile
+    next = saved(k + 1);
+    umma::cp_async_wait<kGrStages - 2>();
+    __syncwarp();
+    fetch(k + kGrStages - 1);
+    const T* xs = ring + k % kGrStages * Shape::kSlot + 2 * lane;
+    F2 a[S], n[S], xv[S], d[S];
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      const bool in = t0 + s < end;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const Gate gt = gate_of(gr[s].get(v));
-        a[s][v] = in ? gt.a : 1.0f;
-        n[s][v] = in ? gt.n : 0.0f;
-        x[s][v] = in ? xr[s].get(v) : 0.0f;
-        d[s][v] = in ? dr[s].get(v) : 0.0f;
-        f.H[v] = fmaf(a[s][v], f.H[v], n[s][v] * x[s][v]);
-        f.A[v] *= a[s][v];
-      }
+      const Gate2 gt = gate_of(load_pair(xs + (S + s) * kGrCols));
+      a[s] = gt.a;
+      n[s] = gt.n;
+      xv[s] = load_pair(xs + s * kGrCols);
+      d[s] = load_pair(xs + (2 * S + s) * kGrCols);
     }
-    float h[V];
+    if (t0 + S > end) {  // past the end: the identity (x and dy were copied as zero)
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      h[v] = hc[v];
-      q.A[v] = f.A[v];
+      for (int s = 0; s < S; ++s)
+        if (t0 + s >= end) {
+          a[s] = f2(1.0f, 1.0f);
+          n[s] = zero;
+        }
     }
+    GrMap f = map_one(), q;
 #pragma unroll
-    for (int s = S - 1; s >= 0; --s)
+    for (int s = 0; s < S; ++s) map_then(f, GrMap{a[s], n[s] * xv[s]});
+    q.A = f.A;
+    q.H = zero;
 #pragma unroll
-      for (int v = 0; v < V; ++v) q.H[v] = a[s][v] * (q.H[v] + d[s][v]);
-    if (k + 1 < rounds) fetch(t0 - p.N * kTile);
-    map_store<V>(&fwd[k & 1][w][lane * 2 * V], f);
+    for (int s = S - 1; s >= 0; --s) q.H = a[s] * (q.H + d[s]);
+    map_store(&fwd[k & 1][w][lane], f);
     // the scan runs from the last token: positions count from the end
-    float e[V];
-    gr_round<V>(sh, k & 1, kGrWarps - 1 - w, p.N - 1 - rank, p.N, lane, q, l, e,
-                [&](int r) { return p.N - 1 - r; });
-    for (int i = 0; i < w; ++i) map_apply<V>(h, map_load<V>(&fwd[k & 1][i][lane * 2 * V]));
+    F2 e;
+    ok = gr_round(sh, k, kGrWarps - 1 - w, p.N - 1 - rank, p.N, lane, q, l, e, ok,
+                  [&](int r) { return p.N - 1 - r; });
+    if (live) {
+      for (int i = 0; i < w; ++i) map_apply(h, map_load(&fwd[k & 1][i][lane]));
 #pragma unroll
-    for (int s = 0; s < S; ++s)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float u = n[s][v] * x[s][v];
-        x[s][v] = h[v] - x[s][v];
-        h[v] = fmaf(a[s][v], h[v], u);
+      for (int s = 0; s < S; ++s) {
+        const F2 u = n[s] * xv[s];
+        xv[s] = f2_fma(xv[s], minus, h);  // h_{t-1} - x_t
+        h = f2_fma(a[s], h, u);
       }
+      const size_t at = seq + (size_t)t0 * p.D + c;
+      float *dx = p.dx + at, *dg = p.dg + at;
 #pragma unroll
-    for (int s = S - 1; s >= 0; --s) {
-      float dx[V], dg[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float lt = e[v] + d[s][v];
-        dx[v] = n[s][v] * lt;  // past the end n is 0
-        e[v] = a[s][v] * lt;
-        dg[v] = dx[v] * x[s][v] * a[s][v];
-      }
-      if (live && t0 + s < p.L) {
-        const size_t at = base + (size_t)(t0 + s) * p.D;
-        store_f32<V>(p.dx + at, dx);
-        store_f32<V>(p.dg + at, dg);
+      for (int s = S - 1; s >= 0; --s) {
+        const F2 lt = e + d[s];
+        const F2 dxv = n[s] * lt;  // past the end n is 0
+        e = a[s] * lt;
+        if (t0 + s < p.L) {
+          gr_store<kPair>(dx + (size_t)s * p.D, dxv, two);
+          gr_store<kPair>(dg + (size_t)s * p.D, dxv * xv[s] * a[s], two);
+        }
       }
     }
   }
+  gr_cluster_end(p.N, ok);
   if (p.dh0) {
-    __syncthreads();  // dh0 may be dh_last, as above
-    if (live && rank == 0 && w == 0) store_f32<V>(p.dh0 + (size_t)b * p.D + c, l);
+    if (live && rank == 0 && w == 0) gr_store<kPair>(p.dh0 + (size_t)b * p.D + c, l, two);
   }
 }
 

@@ -158,23 +158,21 @@ based_status_t check_gatedrec(const void* x, const void* g, const void* y, const
   return BASED_OK;
 }
 
-// Runs f(T{}, integral_constant<V>) with the channels per lane.
+// Runs f(T{}, integral_constant<CW>) with the copy size: the widest of 16, 8, 4
+// and 2 bytes that divides a row of D values.
 template <typename F>
-based_status_t for_channels(based_dtype_t dt, int D, F f) {
-  using std::integral_constant;
-  if (dt == BASED_F32)
-    return D % 2 == 0 ? f(float{}, integral_constant<int, 2>{})
-                      : f(float{}, integral_constant<int, 1>{});
-  return D % 2 == 0 ? f(__nv_bfloat16{}, integral_constant<int, 2>{})
-                    : f(__nv_bfloat16{}, integral_constant<int, 1>{});
+based_status_t for_copies(based_dtype_t dt, int D, F f) {
+  return for_vector(dt, D, [&](auto t, auto v) {
+    using T = decltype(t);
+    return f(T{}, std::integral_constant<int, decltype(v)::value * (int)sizeof(T)>{});
+  });
 }
 
 // Launches kern on B * n_blk clusters of N CTAs, as a dependent launch.
 template <typename P>
-bool launch_gatedrec(void (*kern)(P), const P& p, long long clusters, cudaStream_t st) {
-  if (p.N > 8 &&
-      cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-    return false;
+bool launch_gatedrec(void (*kern)(P), const P& p, long long clusters, size_t smem,
+                     cudaStream_t st) {
+  if (!set_smem(kern, smem)) return false;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -185,6 +183,7 @@ bool launch_gatedrec(void (*kern)(P), const P& p, long long clusters, cudaStream
   attr[1].val.clusterDim.z = 1;
   cfg.gridDim = dim3((unsigned)(clusters * p.N));
   cfg.blockDim = dim3(kGrThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = p.N > 1 ? 2 : 1;
@@ -321,13 +320,13 @@ based_status_t based_gatedrec_fwd(const void* x, const void* g, void* y, const f
   GrFwdParams p{};
   p.x = x; p.g = g; p.y = y; p.h0 = h0; p.h_last = h_last; p.h_chunks = h_chunks;
   p.lengths = lengths; p.L = L; p.D = D;
-  return for_channels(dt, D, [&](auto t, auto v) -> based_status_t {
+  return for_copies(dt, D, [&](auto t, auto cw) -> based_status_t {
     using T = decltype(t);
-    constexpr int V = decltype(v)::value;
-    p.n_blk = (int)ceil_div(D, 32 * V);
+    p.n_blk = (int)ceil_div(D, kGrCols);
     const long long clusters = (long long)B * p.n_blk;
-    p.N = gatedrec_cluster(clusters, L, GrShape<T, V>::kTile);
-    if (!launch_gatedrec(gatedrec_fwd_kernel<T, V>, p, clusters, static_cast<cudaStream_t>(stream)))
+    p.N = gatedrec_cluster(clusters, L, GrFwdShape<T>::kTile);
+    if (!launch_gatedrec(gatedrec_fwd_kernel<T, decltype(cw)::value>, p, clusters,
+                         GrFwdShape<T>::kSmem, static_cast<cudaStream_t>(stream)))
       return BASED_ERR_CUDA;
     return launch_status();
   });
@@ -348,13 +347,13 @@ based_status_t based_gatedrec_bwd(const void* x, const void* g, const void* dy,
   GrBwdParams p{};
   p.x = x; p.g = g; p.dy = dy; p.h_chunks = h_chunks; p.dh_last = dh_last;
   p.dx = dx; p.dg = dg; p.dh0 = dh0; p.lengths = lengths; p.L = L; p.D = D;
-  return for_channels(dt, D, [&](auto t, auto v) -> based_status_t {
+  return for_copies(dt, D, [&](auto t, auto cw) -> based_status_t {
     using T = decltype(t);
-    constexpr int V = decltype(v)::value;
-    p.n_blk = (int)ceil_div(D, 32 * V);
+    p.n_blk = (int)ceil_div(D, kGrCols);
     const long long clusters = (long long)B * p.n_blk;
     p.N = gatedrec_cluster(clusters, L, kGrChunk);
-    if (!launch_gatedrec(gatedrec_bwd_kernel<T, V>, p, clusters, static_cast<cudaStream_t>(stream)))
+    if (!launch_gatedrec(gatedrec_bwd_kernel<T, decltype(cw)::value>, p, clusters,
+                         GrBwdShape<T>::kSmem, static_cast<cudaStream_t>(stream)))
       return BASED_ERR_CUDA;
     return launch_status();
   });

@@ -127,6 +127,13 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool vali
                "r"(valid ? 16 : 0)
                : "memory");
 }
+// The same for 4 or 8 bytes (aligned to their size).
+template <int Bytes>
+__device__ __forceinline__ void cp_async_small(void* dst, const void* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(valid ? Bytes : 0), "n"(Bytes)
+               : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
@@ -509,6 +516,35 @@ __device__ __forceinline__ void tmem_relinquish_pair() {
 __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
                : "memory");
+}
+// Store 16 bytes at shared::cluster address `dst` of any CTA of the cluster and
+// complete 16 transaction bytes on that CTA's mbarrier `bar` (shared::cluster
+// address): no fence, and nothing of this thread is waited for.
+__device__ __forceinline__ void st_async_16(uint32_t dst, uint64_t a, uint64_t b, uint32_t bar) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::"r"(
+          dst),
+      "l"(a), "l"(b), "r"(bar)
+      : "memory");
+}
+// Bounded wait for a phase that CTAs of the cluster complete (as mbar_wait_cluster,
+// without a call, for kernels that hold many registers across it).
+__device__ __forceinline__ bool mbar_wait_cluster_inline(uint64_t* bar, uint32_t parity) {
+  uint64_t t0 = 0;
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    const uint64_t now = global_timer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > *const_cast<const volatile uint64_t*>(&g_wait_limit_ns)) return false;
+  }
 }
 // Arrive on an mbarrier of either CTA (shared::cluster address), releasing this
 // thread's prior writes at cluster scope.
