@@ -36,16 +36,35 @@ inline int row_warps_for(int D, int E) {
   return w;
 }
 
+// Threads of a CTA for rows of row_warps warps.
+inline int row_threads(int row_warps) {
+  return row_warps * 32 > kLnThreads ? row_warps * 32 : kLnThreads;
+}
+
 template <typename T, int V, int E>
 based_status_t launch_layernorm_fwd(LnFwdParams p, cudaStream_t st) {
   p.row_warps = row_warps_for(p.D, E);
-  const int tpr = p.row_warps * 32, threads = tpr > kLnThreads ? tpr : kLnThreads;
-  const long long blocks = ceil_div(p.rows, threads / tpr);
-  if (blocks > 0x7fffffffLL) return BASED_ERR_UNSUPPORTED;
-  if (!launch_dependent(layernorm_fwd_kernel<T, V, E>, dim3((unsigned)blocks), dim3(threads), 0, st,
-                        p))
-    return BASED_ERR_CUDA;
-  return launch_status();
+  const int threads = row_threads(p.row_warps);
+  const long long want = ceil_div(p.rows, threads / (p.row_warps * 32));
+  const long long most = 2LL * device_sm_count();
+  const dim3 grid((unsigned)(want < most ? want : most));
+  auto go = [&](auto kern) -> based_status_t {
+    if (!launch_dependent(kern, grid, dim3(threads), 0, st, p)) return BASED_ERR_CUDA;
+    return launch_status();
+  };
+  auto pick = [&](auto n) {
+    constexpr int kN = decltype(n)::value;
+    return p.residual ? go(layernorm_fwd_kernel<T, V, E, true, kN>)
+                      : go(layernorm_fwd_kernel<T, V, E, false, kN>);
+  };
+  using std::integral_constant;
+  if constexpr (E > 8) {
+    if (threads == 512) return pick(integral_constant<int, 512>{});
+  }
+  if constexpr (E == 16) {
+    if (threads == 1024) return pick(integral_constant<int, 1024>{});
+  }
+  return pick(integral_constant<int, 256>{});
 }
 
 struct LnBwdPlan {
@@ -55,9 +74,8 @@ LnBwdPlan plan_layernorm_bwd(long long rows, int D) {
   LnBwdPlan pl;
   pl.E = D <= 256 ? 8 : 16;
   pl.row_warps = row_warps_for(D, pl.E);
-  const int tpr = pl.row_warps * 32;
-  pl.threads = tpr > kLnThreads ? tpr : kLnThreads;
-  const long long want = ceil_div(rows, pl.threads / tpr);
+  pl.threads = row_threads(pl.row_warps);
+  const long long want = ceil_div(rows, pl.threads / (pl.row_warps * 32));
   const long long most = 2LL * device_sm_count();
   pl.parts = (int)(want < most ? want : most);
   return pl;
@@ -66,13 +84,26 @@ LnBwdPlan plan_layernorm_bwd(long long rows, int D) {
 template <typename T, int V, int E>
 based_status_t launch_layernorm_bwd(LnBwdParams p, const LnBwdPlan& pl, float* dw, float* db,
                                     cudaStream_t st) {
-  auto kern = layernorm_bwd_kernel<T, V, E>;
-  const size_t smem = pl.row_warps * 32 < pl.threads ? (size_t)p.D * 8 : 0;
-  if (!set_smem(kern, smem)) return BASED_ERR_CUDA;
   p.row_warps = pl.row_warps;
-  if (pl.parts > 0 &&
-      !launch_dependent(kern, dim3((unsigned)pl.parts), dim3(pl.threads), smem, st, p))
-    return BASED_ERR_CUDA;
+  if (pl.parts > 0) {
+    auto go = [&](auto n) {
+      constexpr int kN = decltype(n)::value;
+      auto kern = layernorm_bwd_kernel<T, V, E, kN>;
+      const size_t smem = LnBwdShape<T, V, E, kN>::smem(pl.row_warps * 32, p.D);
+      return set_smem(kern, smem) &&
+             launch_dependent(kern, dim3((unsigned)pl.parts), dim3(kN), smem, st, p);
+    };
+    using std::integral_constant;
+    bool ok;
+    if constexpr (E > 8) {
+      ok = pl.threads == 256   ? go(integral_constant<int, 256>{})
+           : pl.threads == 512 ? go(integral_constant<int, 512>{})
+                               : go(integral_constant<int, 1024>{});
+    } else {
+      ok = go(integral_constant<int, 256>{});
+    }
+    if (!ok) return BASED_ERR_CUDA;
+  }
   if (!launch_dependent(layernorm_parts_kernel, dim3((unsigned)ceil_div(2LL * p.D, 32)),
                         dim3(32, 32), 0, st, (const float*)p.parts, pl.parts, p.D, dw, db))
     return BASED_ERR_CUDA;
@@ -226,7 +257,8 @@ based_status_t based_layernorm_fwd(const void* x, const void* residual, const fl
   return for_vector(dt, D, [&](auto t, auto v) {
     using T = decltype(t);
     constexpr int V = decltype(v)::value;
-    return D <= 256 ? launch_layernorm_fwd<T, V, 8>(p, st) : launch_layernorm_fwd<T, V, 32>(p, st);
+    return D <= 256 ? launch_layernorm_fwd<T, V, 8>(p, st)
+                    : launch_layernorm_fwd<T, V, (V >= 4 ? 32 : 16)>(p, st);
   });
 }
 
@@ -258,7 +290,7 @@ based_status_t based_layernorm_bwd(const void* dy, const void* x, const float* w
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   return for_vector(dt, D, [&](auto t, auto v) {
     using T = decltype(t);
-    constexpr int V = decltype(v)::value;
+    constexpr int V = decltype(v)::value < 4 ? decltype(v)::value : 4;
     return pl.E == 8 ? launch_layernorm_bwd<T, V, 8>(p, pl, dweight, dbias, st)
                      : launch_layernorm_bwd<T, V, 16>(p, pl, dweight, dbias, st);
   });

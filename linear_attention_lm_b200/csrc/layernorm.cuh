@@ -18,12 +18,13 @@
 
 namespace based {
 
-constexpr int kLnThreads = 256;   // threads of a CTA (more only for rows of over 8192 values)
+constexpr int kLnThreads = 256;   // threads of a CTA (more only for the longest rows)
 constexpr int kLnMaxD = 16384;
 
-// Sums of N values over the threads of a row: row_warps warps of the CTA, warp
-// index in the row wr.  Every thread of the CTA calls it; `red` holds
-// N floats per warp and is free again after the caller's next barrier.
+// Sums of N values over the threads of a row: row_warps warps of the CTA, this
+// one the wr-th.  `red` holds N floats per warp and is free again after the
+// row's next barrier.  Rows of several warps have a named barrier of their own,
+// so the rows of a CTA run at their own pace.
 template <int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], float* red, int warp, int wr,
                                         int row_warps) {
@@ -34,7 +35,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* red, int warp, int
 #pragma unroll
     for (int n = 0; n < N; ++n) red[warp * N + n] = v[n];
   }
-  __syncthreads();
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / row_warps), "r"(row_warps * 32) : "memory");
   const float* r = red + (warp - wr) * N;
 #pragma unroll
   for (int n = 0; n < N; ++n) {
@@ -54,83 +55,86 @@ struct LnFwdParams {
   float eps;
 };
 
-// One row per row_warps warps, E values per thread in vectors of V.
-template <typename T, int V, int E>
-__global__ void __launch_bounds__(512) layernorm_fwd_kernel(const LnFwdParams p) {
+// E values per thread in vectors of V; a group of row_warps warps takes every
+// (number of groups)-th row and loads the next one before it works on this one.
+template <typename T, int V, int E, bool kResidual, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
+    layernorm_fwd_kernel(const LnFwdParams p) {
   constexpr int NV = E / V;
-  __shared__ float red[2][16];
+  __shared__ float red[2][32];
   const int warp = threadIdx.x >> 5, wr = warp % p.row_warps;
   const int lane = threadIdx.x - (warp - wr) * 32;  // thread index in the row
-  const int tpr = p.row_warps * 32;
-  const long long row =
-      (long long)blockIdx.x * (blockDim.x / tpr) + warp / p.row_warps;
-  const bool live = row < p.rows;
-  const size_t off = live ? (size_t)row * p.D : 0;
+  const int tpr = p.row_warps * 32, rpb = blockDim.x / tpr;
+  const float inv_d = 1.0f / p.D;
   umma::grid_dep_wait();
 
-  float f[NV][V];
-  Pack<T, V> a[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * tpr + lane) * V;
-    a[i].zero();
-    if (live && c < p.D) a[i].load(static_cast<const T*>(p.x) + off + c);
-  }
-  if (p.residual) {
-    Pack<T, V> b[NV];
+  Pack<T, V> x[NV], r[NV];
+  auto fetch = [&](long long row) {
+    const size_t off = (size_t)row * p.D;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * tpr + lane) * V;
-      b[i].zero();
-      if (live && c < p.D) b[i].load(static_cast<const T*>(p.residual) + off + c);
+      if (c < p.D) {
+        x[i].load(static_cast<const T*>(p.x) + off + c);
+        if (kResidual) r[i].load(static_cast<const T*>(p.residual) + off + c);
+      }
+    }
+  };
+  long long row = (long long)blockIdx.x * rpb + warp / p.row_warps;
+  const long long step = (long long)gridDim.x * rpb;
+  if (row < p.rows) fetch(row);
+  for (; row < p.rows; row += step) {
+    const size_t off = (size_t)row * p.D;
+    float f[NV][V];
+    float sum[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * tpr + lane) * V;
+      const bool in = c < p.D;
+      if (kResidual) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) x[i].set(e, x[i].get(e) + r[i].get(e));
+        if (in) x[i].store(static_cast<T*>(p.resid_out) + off + c);
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        f[i][e] = in ? x[i].get(e) : 0.0f;
+        sum[0] += f[i][e];
+      }
+    }
+    if (row + step < p.rows) fetch(row + step);
+    row_sum<1>(sum, red[0], warp, wr, p.row_warps);
+    const float mean = sum[0] * inv_d;
+    float sq[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const bool in = (i * tpr + lane) * V < p.D;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        f[i][e] = in ? f[i][e] - mean : 0.0f;
+        sq[0] += f[i][e] * f[i][e];
+      }
+    }
+    row_sum<1>(sq, red[1], warp, wr, p.row_warps);
+    const float rstd = 1.0f / sqrtf(sq[0] * inv_d + p.eps);
+    if (lane == 0) {
+      if (p.mean) p.mean[row] = mean;
+      if (p.rstd) p.rstd[row] = rstd;
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * tpr + lane) * V;
+      if (c < p.D) {
+        float w[V], b[V];
+        load_f32<V>(p.w + c, w);
 #pragma unroll
-      for (int e = 0; e < V; ++e) a[i].set(e, a[i].get(e) + b[i].get(e));
-      if (live && c < p.D) a[i].store(static_cast<T*>(p.resid_out) + off + c);
-    }
-  }
-  float sum[1] = {0.0f};
+        for (int e = 0; e < V; ++e) b[e] = 0.0f;
+        if (p.b) load_f32<V>(p.b + c, b);
+        Pack<T, V> y;
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      f[i][e] = a[i].get(e);
-      sum[0] += f[i][e];
-    }
-  row_sum<1>(sum, red[0], warp, wr, p.row_warps);
-  const float mean = sum[0] / p.D;
-  float sq[1] = {0.0f};
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const bool in = (i * tpr + lane) * V < p.D;
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      f[i][e] = in ? f[i][e] - mean : 0.0f;
-      sq[0] += f[i][e] * f[i][e];
-    }
-  }
-  row_sum<1>(sq, red[1], warp, wr, p.row_warps);
-  const float rstd = 1.0f / sqrtf(sq[0] / p.D + p.eps);
-  if (!live) return;
-  if (lane == 0) {
-    if (p.mean) p.mean[row] = mean;
-    if (p.rstd) p.rstd[row] = rstd;
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * tpr + lane) * V;
-    if (c < p.D) {
-      float w[V], b[V];
-      load_f32<V>(p.w + c, w);
-#pragma unroll
-      for (int e = 0; e < V; ++e) b[e] = 0.0f;
-      if (p.b) load_f32<V>(p.b + c, b);
-#pragma unroll
-      for (int e = 0; e < V; ++e) a[i].set(e, fmaf(f[i][e] * rstd, w[e], b[e]));
-      a[i].store(static_cast<T*>(p.y) + off + c);
+        for (int e = 0; e < V; ++e) y.set(e, fmaf(f[i][e] * rstd, w[e], b[e]));
+        y.store(static_cast<T*>(p.y) + off + c);
+      }
     }
   }
 }
@@ -143,13 +147,39 @@ struct LnBwdParams {
   int D, row_warps;
 };
 
-// CTA i takes rows i*rpb, i*rpb + gridDim*rpb, ...; a thread owns its columns
-// for all of them and sums dweight and dbias in registers; the row groups of the
-// CTA meet in shared memory, and the CTA writes one part [2][D] (fp32).
-template <typename T, int V, int E>
-__global__ void __launch_bounds__(1024) layernorm_bwd_kernel(const LnBwdParams p) {
-  constexpr int NV = E / V;
-  extern __shared__ float smem[];
+// A thread owns its columns for all the rows of its group and sums dweight and
+// dbias in registers; the groups of the CTA meet in shared memory at the end, and
+// the CTA writes one part [2][D] (fp32).  Vectors are four values at most: 16
+// bytes of the fp32 arrays, which are most of the traffic.  The rows to come are
+// copied ahead by cp.async into slots that only the copying thread reads, so no
+// barrier is between a row's arrival and its use.
+template <typename T, int V, int E, int kThreads>
+struct LnBwdShape {
+  static constexpr int NV = E / V;
+  // two-byte copies have no asynchronous form, and the longest rows no room
+  static constexpr bool kAsync = V * sizeof(T) >= 4 && kThreads <= 512;
+  static constexpr int kStages = sizeof(T) == 2 ? 3 : 2;  // two CTAs of 256 threads fit an SM
+  static constexpr int kX = V * (int)sizeof(T), kR = V * 4;  // bytes of a vector
+  static constexpr int kThread = NV * (2 * kX + kR);         // bytes of a thread's row
+  static size_t smem(int tpr, int D) {
+    const size_t ring = kAsync ? (size_t)kStages * kThread * kThreads : 0;
+    const size_t join = tpr < kThreads ? (size_t)D * 8 : 0;
+    return ring > join ? ring : join;
+  }
+};
+
+template <int Bytes>
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+  if constexpr (Bytes == 16) umma::cp_async16(to, from, true);
+  else umma::cp_async_small<Bytes>(to, from, true);
+}
+
+template <typename T, int V, int E, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 256 && E <= 16 ? 2 : 1)
+    layernorm_bwd_kernel(const LnBwdParams p) {
+  using Shape = LnBwdShape<T, V, E, kThreads>;
+  constexpr int NV = Shape::NV, kStages = Shape::kStages;
+  extern __shared__ __align__(16) unsigned char ln_smem[];
   __shared__ float red[2][64];
   const int warp = threadIdx.x >> 5, wr = warp % p.row_warps;
   const int lane = threadIdx.x - (warp - wr) * 32;
@@ -164,37 +194,74 @@ __global__ void __launch_bounds__(1024) layernorm_bwd_kernel(const LnBwdParams p
     for (int e = 0; e < V; ++e) w[i][e] = dw[i][e] = db[i][e] = 0.0f;
     if (c < p.D) load_f32<V>(p.w + c, w[i]);
   }
+  // slot of (stage, array, vector i): [thread] vectors
+  auto slot = [&](int stage, int array, int i) {
+    unsigned char* s = ln_smem + (size_t)stage * Shape::kThread * blockDim.x;
+    return s + (array * NV * Shape::kX + i * (array == 2 ? Shape::kR : Shape::kX)) * blockDim.x +
+           threadIdx.x * (array == 2 ? Shape::kR : Shape::kX);
+  };
+  const T *x = static_cast<const T*>(p.x), *dy = static_cast<const T*>(p.dy);
+  auto fetch = [&](long long row, int stage) {
+    if (row < p.rows) {
+      const size_t off = (size_t)row * p.D;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + lane) * V;
+        if (c < p.D) {
+          copy_async<Shape::kX>(slot(stage, 0, i), x + off + c);
+          copy_async<Shape::kX>(slot(stage, 1, i), dy + off + c);
+          if (p.dresid) copy_async<Shape::kR>(slot(stage, 2, i), p.dresid + off + c);
+        }
+      }
+    }
+    umma::cp_async_commit();
+  };
   const float inv_d = 1.0f / p.D;
-  int buf = 0;
-  for (long long r0 = (long long)blockIdx.x * rpb; r0 < p.rows; r0 += (long long)gridDim.x * rpb) {
-    const long long row = r0 + warp / p.row_warps;
-    const bool live = row < p.rows;
-    const size_t off = live ? (size_t)row * p.D : 0;
-    const float mean = live ? p.mean[row] : 0.0f, rstd = live ? p.rstd[row] : 0.0f;
-    Pack<T, V> x[NV], g[NV];
-    float s[2] = {0.0f, 0.0f};
+  const long long step = (long long)gridDim.x * rpb;
+  long long row = (long long)blockIdx.x * rpb + warp / p.row_warps;
+  if constexpr (Shape::kAsync) {
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) fetch(row + k * step, k);
+  }
+  float mean = 0.0f, rstd = 0.0f;
+  if (row < p.rows) mean = p.mean[row], rstd = p.rstd[row];
+  int buf = 0, stage = 0;
+  for (; row < p.rows; row += step) {
+    const size_t off = (size_t)row * p.D;
+    float next_mean = 0.0f, next_rstd = 0.0f;
+    if (row + step < p.rows) next_mean = p.mean[row + step], next_rstd = p.rstd[row + step];
+    Pack<T, V> xv[NV], gv[NV];
+    if constexpr (Shape::kAsync) umma::cp_async_wait<kStages - 2>();
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * tpr + lane) * V;
-      x[i].zero();
-      g[i].zero();
-      if (live && c < p.D) {
-        x[i].load(static_cast<const T*>(p.x) + off + c);
-        g[i].load(static_cast<const T*>(p.dy) + off + c);
+      xv[i].zero();
+      gv[i].zero();
+      if (c < p.D) {
+        if constexpr (Shape::kAsync) {
+          xv[i].load(reinterpret_cast<const T*>(slot(stage, 0, i)));
+          gv[i].load(reinterpret_cast<const T*>(slot(stage, 1, i)));
+        } else {
+          xv[i].load(x + off + c);
+          gv[i].load(dy + off + c);
+        }
       }
     }
+    // into the slot of the row before
+    if constexpr (Shape::kAsync)
+      fetch(row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
+    float s[2] = {0.0f, 0.0f};
     float xh[NV][V];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float gv = g[i].get(e);
-        xh[i][e] = (x[i].get(e) - mean) * rstd;
-        const float t = gv * w[i][e];
+        const float g = gv[i].get(e), t = g * w[i][e];
+        xh[i][e] = (xv[i].get(e) - mean) * rstd;
         s[0] += t;
         s[1] += t * xh[i][e];
-        dw[i][e] += gv * xh[i][e];
-        db[i][e] += gv;
+        dw[i][e] += g * xh[i][e];
+        db[i][e] += g;
       }
     row_sum<2>(s, red[buf], warp, wr, p.row_warps);
     buf ^= 1;
@@ -202,20 +269,28 @@ __global__ void __launch_bounds__(1024) layernorm_bwd_kernel(const LnBwdParams p
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * tpr + lane) * V;
-      if (live && c < p.D) {
+      if (c < p.D) {
         float o[V], d[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) d[e] = 0.0f;
-        if (p.dresid) load_f32<V>(p.dresid + off + c, d);
+        if (p.dresid)
+          load_f32<V>(Shape::kAsync ? reinterpret_cast<const float*>(slot(stage, 2, i))
+                                    : p.dresid + off + c,
+                      d);
 #pragma unroll
         for (int e = 0; e < V; ++e)
-          o[e] = fmaf(rstd, g[i].get(e) * w[i][e] - c0 - xh[i][e] * c1, d[e]);
+          o[e] = fmaf(rstd, gv[i].get(e) * w[i][e] - c0 - xh[i][e] * c1, d[e]);
         store_f32<V>(p.dx + off + c, o);
       }
     }
+    mean = next_mean;
+    rstd = next_rstd;
+    stage = stage + 1 == kStages ? 0 : stage + 1;
   }
+  if constexpr (Shape::kAsync) umma::cp_async_wait<0>();
   // rows of the CTA together: group 0 adds the others' sums in order
   float* part = p.parts + (size_t)blockIdx.x * 2 * p.D;
+  float* join = reinterpret_cast<float*>(ln_smem);
   for (int grp = rpb - 1; grp > 0; --grp) {
     __syncthreads();
     if (warp / p.row_warps == grp) {
@@ -225,8 +300,8 @@ __global__ void __launch_bounds__(1024) layernorm_bwd_kernel(const LnBwdParams p
         if (c < p.D)
 #pragma unroll
           for (int e = 0; e < V; ++e) {
-            smem[c + e] = dw[i][e];
-            smem[p.D + c + e] = db[i][e];
+            join[c + e] = dw[i][e];
+            join[p.D + c + e] = db[i][e];
           }
       }
     }
@@ -238,8 +313,8 @@ __global__ void __launch_bounds__(1024) layernorm_bwd_kernel(const LnBwdParams p
         if (c < p.D)
 #pragma unroll
           for (int e = 0; e < V; ++e) {
-            dw[i][e] += smem[c + e];
-            db[i][e] += smem[p.D + c + e];
+            dw[i][e] += join[c + e];
+            db[i][e] += join[p.D + c + e];
           }
       }
     }
