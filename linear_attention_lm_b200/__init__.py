@@ -495,6 +495,9 @@ def _arg(t, shape, dtype, name: str, device: torch.device):
     contiguous and sit on this device (None stays None)."""
     if t is None:
         return None
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device.index
+            and t.shape == shape and t.is_contiguous()):
+        return t.data_ptr() or None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.shape != shape:
@@ -503,9 +506,33 @@ def _arg(t, shape, dtype, name: str, device: torch.device):
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr() or None
+    raise ValueError(f"{name} must be contiguous")
+
+
+# the current stream's handle without a stream object around it
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _run(fn: str, args, stream, device: torch.device):
+    """Call an entry point whose last argument is the stream, with the tensors'
+    device current (these calls can be as short as their launch: nothing is
+    switched or wrapped that need not be)."""
+    if isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream
+    elif stream is not None:
+        handle = int(stream)
+    elif _current_raw_stream is not None:
+        handle = _current_raw_stream(device.index)
+    else:
+        handle = torch.cuda.current_stream(device).cuda_stream
+    call = getattr(_lib or load_library(), fn)
+    if torch.cuda.current_device() == device.index:
+        st = call(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            st = call(*args, handle)
+    if st != 0:
+        raise BasedError(fn, st)
 
 
 def _required(**ts):
@@ -533,10 +560,7 @@ def based_layernorm_fwd(x, weight, bias, y, eps: float = 1e-5, residual=None, re
             _arg(weight, (D,), f32, "weight", dev), _arg(bias, (D,), f32, "bias", dev),
             _arg(y, shape, dtype, "y", dev), _arg(resid_out, shape, dtype, "resid_out", dev),
             _arg(mean, lead, f32, "mean", dev), _arg(rstd, lead, f32, "rstd", dev))
-    with torch.cuda.device(dev):
-        st = load_library().based_layernorm_fwd(*args, lead.numel(), D, dt, float(eps),
-                                                _torch_stream(stream, dev).cuda_stream)
-    _check("based_layernorm_fwd", st)
+    _run("based_layernorm_fwd", (*args, lead.numel(), D, dt, float(eps)), stream, dev)
     return y
 
 
@@ -566,13 +590,14 @@ def based_layernorm_bwd(dy, x, weight, mean, rstd, dx, dweight, dbias, dresid=No
             _arg(rstd, lead, f32, "rstd", dev), _arg(dresid, shape, f32, "dresid", dev),
             _arg(dx, shape, f32, "dx", dev), _arg(dweight, (D,), f32, "dweight", dev),
             _arg(dbias, (D,), f32, "dbias", dev))
-    ts = _torch_stream(stream, dev)
-    with torch.cuda.device(dev):
-        nbytes = based_layernorm_bwd_workspace_bytes(rows, D) if workspace is None else 0
-        workspace, ws_bytes = _workspace(nbytes, workspace, dev, ts, "based_layernorm_bwd")
-        st = load_library().based_layernorm_bwd(*args, rows, D, dt, _ptr(workspace), ws_bytes,
-                                                ts.cuda_stream)
-    _check("based_layernorm_bwd", st)
+    if workspace is None:
+        stream = _torch_stream(stream, dev)
+        with torch.cuda.device(dev):
+            nbytes = based_layernorm_bwd_workspace_bytes(rows, D)
+            workspace, ws_bytes = _workspace(nbytes, None, dev, stream, "based_layernorm_bwd")
+    else:
+        workspace, ws_bytes = _workspace(0, workspace, dev, None, "based_layernorm_bwd")
+    _run("based_layernorm_bwd", (*args, rows, D, dt, _ptr(workspace), ws_bytes), stream, dev)
     return dx, dweight, dbias
 
 
@@ -623,13 +648,7 @@ def _rotary(fn, q, k, q_out, k_out, freqs, pos, layout, mscale, dtype, stream):
             ROTARY_LAYOUTS[layout], float(mscale))
     if per_seq and B == 0:
         return q_out, k_out
-    with torch.cuda.device(dev):
-        handle = _torch_stream(stream, dev).cuda_stream
-        if fn == "based_rotary_fwd":
-            st = load_library().based_rotary_fwd(*args, dt, handle)
-        else:
-            st = load_library().based_rotary_bwd(*args, handle)
-    _check(fn, st)
+    _run(fn, (*args, dt) if fn == "based_rotary_fwd" else args, stream, dev)
     return q_out, k_out
 
 
@@ -673,10 +692,7 @@ def based_gatedrec_fwd(x, g, y, h0=None, h_last=None, h_chunks=None, lengths=Non
             _arg(y, x.shape, x.dtype, "y", dev), _arg(h0, (B, D), f32, "h0", dev),
             _arg(h_last, (B, D), f32, "h_last", dev), _arg(h_chunks, chunks, f32, "h_chunks", dev),
             _arg(lengths, (B,), torch.int64, "lengths", dev))
-    with torch.cuda.device(dev):
-        st = load_library().based_gatedrec_fwd(*args, B, L, D, dt,
-                                               _torch_stream(stream, dev).cuda_stream)
-    _check("based_gatedrec_fwd", st)
+    _run("based_gatedrec_fwd", (*args, B, L, D, dt), stream, dev)
     return y
 
 
@@ -692,10 +708,7 @@ def based_gatedrec_bwd(x, g, dy, h_chunks, dx, dg, dh_last=None, dh0=None, lengt
             _arg(dh_last, (B, D), f32, "dh_last", dev), _arg(dx, x.shape, f32, "dx", dev),
             _arg(dg, x.shape, f32, "dg", dev), _arg(dh0, (B, D), f32, "dh0", dev),
             _arg(lengths, (B,), torch.int64, "lengths", dev))
-    with torch.cuda.device(dev):
-        st = load_library().based_gatedrec_bwd(*args, B, L, D, dt,
-                                               _torch_stream(stream, dev).cuda_stream)
-    _check("based_gatedrec_bwd", st)
+    _run("based_gatedrec_bwd", (*args, B, L, D, dt), stream, dev)
     return dx, dg, dh0
 
 
@@ -709,10 +722,7 @@ def based_gatedrec_step(x, g, h, y, stream=None):
     dt = _dtype_code(x)
     args = (_arg(x, x.shape, x.dtype, "x", dev), _arg(g, x.shape, x.dtype, "g", dev),
             _arg(h, x.shape, torch.float32, "h", dev), _arg(y, x.shape, x.dtype, "y", dev))
-    with torch.cuda.device(dev):
-        st = load_library().based_gatedrec_step(*args, B, D, dt,
-                                                _torch_stream(stream, dev).cuda_stream)
-    _check("based_gatedrec_step", st)
+    _run("based_gatedrec_step", (*args, B, D, dt), stream, dev)
     return y
 
 
