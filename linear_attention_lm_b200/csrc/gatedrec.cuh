@@ -48,21 +48,21 @@ __device__ __forceinline__ Gate2 gate_of(F2 g2) {
   return Gate2{f2(px ? u.x : t.x, py ? u.y : t.y), f2(px ? t.x : u.x, py ? t.y : u.y)};
 }
 
-// How the sequence is cut: a CTA takes 64 channels, two per lane; a warp S tokens,
-// a CTA kGrWarps warps, one after another (a tile of kGrWarps S tokens), and a
-// cluster of N CTAs walks the sequence N tiles at a time.  Each warp forms its
-// tokens' map h -> A h + H (A the product of its gates, H its end state from
-// zero), the maps of the CTA's warps meet in shared memory and those of the
-// cluster's CTAs in every CTA's shared memory (one cluster barrier per N tiles);
-// then every warp knows the state that enters its tokens and runs them again
-// from its registers.  Inputs are read once: each warp copies its own tokens of
-// the next tiles into a ring of kGrStages slots (cp.async), so loads run ahead of
-// the barriers and hold no registers.
+// How the sequence is cut: a lane takes S tokens of two channels; a warp G groups of
+// lanes, each with the next S tokens of the same 64 / G channels; a CTA kGrWarps
+// warps, one after another (a tile of kGrWarps G S tokens), and a cluster of N CTAs
+// walks the sequence N tiles at a time.  Each lane forms its tokens' map
+// h -> A h + H (A the product of its gates, H its end state from zero); the maps
+// meet in a warp by shuffles, in a CTA in its shared memory and in a cluster in
+// every CTA's shared memory; then every lane knows the state that enters its
+// tokens and runs them again from its registers.  Inputs are read once: each warp
+// copies its own tokens of the next tiles into a ring of kGrStages slots
+// (cp.async), so loads run ahead of the barriers and hold no registers.
 constexpr int kGrWarps = 8;
 constexpr int kGrThreads = 32 * kGrWarps;
-constexpr int kGrCols = 64;
 constexpr int kGrStages = 3;
 constexpr int kGrMaxCluster = 8;
+constexpr int kGrMaxD = 1 << 20;  // 32-bit offsets inside a tile of at most 512 tokens
 
 // A map of two channels per lane in shared memory: A, H of the one, of the other
 struct GrMap {
@@ -80,12 +80,40 @@ __device__ __forceinline__ void map_then(GrMap& m, const GrMap& next) {
   m.H = f2_fma(next.A, m.H, next.H);
   m.A = m.A * next.A;
 }
+// after prev
+__device__ __forceinline__ void map_after(GrMap& m, const GrMap& prev) {
+  m.H = f2_fma(m.A, prev.H, m.H);
+  m.A = m.A * prev.A;
+}
+__device__ __forceinline__ F2 f2_shfl(F2 a, int src) {
+  const float2 v = f2_get(a);
+  return f2(__shfl_sync(0xffffffffu, v.x, src), __shfl_sync(0xffffffffu, v.y, src));
+}
+// The maps of a warp's G groups of lanes in the order of the scan (o: this
+// lane's position; kBack: from the last group): `m` becomes that of the groups up
+// to this one, the result is that of the groups before.
+template <int G, bool kBack>
+__device__ __forceinline__ GrMap map_scan_groups(GrMap& m, int o, int lane) {
+  constexpr int W = 32 / G;
+  if constexpr (G > 1) {
+#pragma unroll
+    for (int d = 1; d < G; d *= 2) {
+      const int src = (kBack ? lane + d * W : lane - d * W) & 31;
+      const GrMap prev{f2_shfl(m.A, src), f2_shfl(m.H, src)};
+      if (o >= d) map_after(m, prev);
+    }
+    const int src = (kBack ? lane + W : lane - W) & 31;
+    const GrMap prev{f2_shfl(m.A, src), f2_shfl(m.H, src)};
+    if (o > 0) return prev;
+  }
+  return map_one();
+}
 __device__ __forceinline__ void map_apply(F2& h, const GrMap& m) { h = f2_fma(m.A, h, m.H); }
 
 // Maps of a CTA's warps and of a cluster's CTAs, two sets in turn.  The CTAs send
 // each other their maps with stores that complete on the receiver's barrier of
 // the set (a cluster barrier would also wait for the outputs' stores to global
-// memory: 29.1 against 27.0 us for 8 x 2048 x 1024 bf16).  A set is written again two rounds later: a CTA
+// memory: 29.1 against 27.0 us at N = 2, 8 x 2048 x 1024 bf16).  A set is written again two rounds later: a CTA
 // sends in round k + 2 when it has received round k + 1 of every CTA, and each
 // sent that when all its warps had read the set of round k.
 struct GrShared {
@@ -94,9 +122,13 @@ struct GrShared {
   uint64_t bar[2];
   uint64_t pad[6];
 };
-__device__ __forceinline__ uint32_t gr_round_bytes(int N) { return (uint32_t)N * 32 * 16; }
+template <int G>
+__device__ __forceinline__ uint32_t gr_round_bytes(int N) {
+  return (uint32_t)N * (32 / G) * 16;
+}
 
 // Before the first round; also: every CTA of the cluster has started.
+template <int G>
 __device__ __forceinline__ void gr_cluster_begin(GrShared& sh, int N) {
   if (N == 1) return;
   if (threadIdx.x == 0) {
@@ -104,7 +136,7 @@ __device__ __forceinline__ void gr_cluster_begin(GrShared& sh, int N) {
     for (int i = 0; i < 2; ++i) umma::mbar_init(&sh.bar[i], 1);
     umma::fence_mbar_init();
 #pragma unroll
-    for (int i = 0; i < 2; ++i) umma::mbar_arrive_expect_tx(&sh.bar[i], gr_round_bytes(N));
+    for (int i = 0; i < 2; ++i) umma::mbar_arrive_expect_tx(&sh.bar[i], gr_round_bytes<G>(N));
   }
   __syncwarp();
   umma::cluster_sync();
@@ -119,69 +151,83 @@ __device__ __forceinline__ void gr_cluster_end(int N, bool ok) {
   else __syncthreads();
 }
 
-// One round k: every warp of the cluster gives its map `mine`; w and r are the
-// positions of the warp in its CTA and of the CTA in its cluster in the order of
-// the scan, to(r) the rank of the CTA at position r.  h: the state that enters
-// the round; on return the state that leaves it, and `enter` the one that enters
-// this warp's tokens.  False: a wait was given up (and every later one is).
-template <typename Rank>
-__device__ __forceinline__ bool gr_round(GrShared& sh, int k, int w, int r, int N, int lane,
-                                         const GrMap& mine, F2& h, F2& enter, bool ok, Rank to) {
-  const int buf = k & 1;
-  map_store(&sh.warp[buf][w][lane], mine);
+// One round k: every lane of the cluster gives its map `mine`.  w, r and o are the
+// positions of the warp in its CTA, of the CTA in its cluster and of the lane's
+// group in its warp in the order of the scan, to(r) the rank of the CTA at
+// position r, l the lane's place in its group.  h: the state that enters the round;
+// on return the state that leaves it, and `enter` the one that enters this lane's
+// tokens.  False: a wait was given up (and every later one is).
+template <int G, bool kBack, typename Rank>
+__device__ __forceinline__ bool gr_round(GrShared& sh, int k, int w, int r, int o, int N, int lane,
+                                         GrMap mine, F2& h, F2& enter, bool ok, Rank to) {
+  const int buf = k & 1, l = lane % (32 / G);
+  const GrMap groups = map_scan_groups<G, kBack>(mine, o, lane);
+  if (G == 1 || o == G - 1) map_store(&sh.warp[buf][w][l], mine);
   __syncthreads();
-  GrMap before = map_one(), all = map_one();
-#pragma unroll
-  for (int i = 0; i < kGrWarps; ++i) {
-    if (i == w) before = all;
-    map_then(all, map_load(&sh.warp[buf][i][lane]));
-  }
   if (N > 1) {
-    if (w < N)
-      umma::st_async_16(umma::cluster_addr(&sh.cta[buf][r][lane], (uint32_t)to(w)), all.A.v,
-                        all.H.v, umma::cluster_addr(&sh.bar[buf], (uint32_t)to(w)));
+    if (w < N) {  // the CTA's map, to the CTA at position w
+      GrMap all = map_load(&sh.warp[buf][0][l]);
+#pragma unroll
+      for (int i = 1; i < kGrWarps; ++i) map_then(all, map_load(&sh.warp[buf][i][l]));
+      if (o == 0)
+        umma::st_async_16(umma::cluster_addr(&sh.cta[buf][r][l], (uint32_t)to(w)), all.A.v, all.H.v,
+                          umma::cluster_addr(&sh.bar[buf], (uint32_t)to(w)));
+    }
     if (ok) ok = umma::mbar_wait_cluster_inline(&sh.bar[buf], (k >> 1) & 1);
-    if (threadIdx.x == 0 && ok) umma::mbar_arrive_expect_tx(&sh.bar[buf], gr_round_bytes(N));  // k + 2
+    if (threadIdx.x == 0 && ok)
+      umma::mbar_arrive_expect_tx(&sh.bar[buf], gr_round_bytes<G>(N));  // for round k + 2
     for (int i = 0; i < N; ++i) {
       if (i == r) enter = h;
-      map_apply(h, map_load(&sh.cta[buf][i][lane]));
+      map_apply(h, map_load(&sh.cta[buf][i][l]));
     }
+    for (int i = 0; i < w; ++i) map_apply(enter, map_load(&sh.warp[buf][i][l]));
   } else {
-    enter = h;
-    map_apply(h, all);
+#pragma unroll
+    for (int i = 0; i < kGrWarps; ++i) {
+      if (i == w) enter = h;
+      map_apply(h, map_load(&sh.warp[buf][i][l]));
+    }
   }
-  map_apply(enter, before);
+  if (G > 1) map_apply(enter, groups);
   return ok;
 }
 static_assert(kGrMaxCluster <= kGrWarps, "warp i sends to the CTA at position i");
 
-// Copies S tokens x 64 channels of a sequence (row length D, from token t0 on) into
-// `slot` [S][64]; tokens from `end` on and channels from `cols` on become zero.
-// CW bytes at a time: the widest size that divides a row.  Rows of an odd number
-// of bf16 have no asynchronous copy and are copied through registers.
-template <typename T, int S, int CW>
+// Copies the G S tokens x 64 / G channels of a warp (row length D, from token t0 on)
+// into `slot`; tokens from `end` on and channels from `cols` on become zero.  Token
+// g S + s lies in row s G + g, so that the G groups of a warp read G rows side by
+// side.  CW bytes at a time: the widest size that divides a row.  Rows of an odd
+// number of bf16 have no asynchronous copy and are copied through registers.
+template <typename T, int S, int G, int CW>
 __device__ __forceinline__ void gr_fetch(T* slot, const T* src, int D, int t0, int end, int cols,
                                          int lane) {
-  constexpr int E = CW / (int)sizeof(T), RC = kGrCols / E;  // elements per copy, copies per row
+  constexpr int kCols = 64 / G;
+  constexpr int E = CW / (int)sizeof(T), RC = kCols / E;  // elements per copy, copies per row
   auto copy = [](T* to, const T* from, bool in) {
     if constexpr (CW == 16) umma::cp_async16(to, from, in);
     else if constexpr (CW >= 4) umma::cp_async_small<CW>(to, from, in);
     else *to = in ? *from : from_f32<T>(0.0f);
   };
-  if (CW == 16 && t0 + S <= end && cols == kGrCols) {
-    const int row = lane / RC, col = lane % RC * E;
-    const T* from = src + ((size_t)(t0 + row) * D + col);
-    T* to = slot + row * kGrCols + col;
+  if constexpr (CW == 16) {  // nothing outside: a start and constant steps
+    constexpr int R = 32 / RC;  // rows per copy instruction
+    static_assert(RC <= 32 && (S % R == 0 || R % S == 0), "the step of a row is a constant");
+    if (t0 + G * S <= end && cols == kCols) {
+      const int row = lane / RC, col = lane % RC * E;
+      const T* from = src + ((size_t)(t0 + row) * D + col);
+      T* to = slot + (row % S * G + row / S) * kCols + col;
+      const size_t step = (size_t)R * D;
 #pragma unroll
-    for (int i = 0; i < S * RC / 32; ++i, from += (size_t)(32 / RC) * D)
-      copy(to + i * (32 / RC) * kGrCols, from, true);
-    return;
+      for (int i = 0; i < S * G / R; ++i, from += step)
+        copy(to + (i * R % S * G + i * R / S) * kCols, from, true);
+      return;
+    }
   }
 #pragma unroll
-  for (int i = 0; i < S * RC / 32; ++i) {
-    const int row = (i * 32 + lane) / RC, col = (i * 32 + lane) % RC * E;
+  for (int i = 0; i < S * 64 / E / 32; ++i) {
+    const int n = i * 32 + lane, row = n / RC, col = n % RC * E;
     const bool in = t0 + row < end && col < cols;
-    copy(slot + row * kGrCols + col, src + (in ? (size_t)(t0 + row) * D + col : 0), in);
+    copy(slot + (row % S * G + row / S) * kCols + col,
+         src + (in ? (size_t)(t0 + row) * D + col : 0), in);
   }
 }
 
@@ -217,36 +263,37 @@ struct GrFwdParams {
   int L, D, n_blk, N;  // n_blk: channel blocks of a sequence; N: CTAs per cluster
 };
 
-template <typename T>
+template <typename T, int G>
 struct GrFwdShape {
   static constexpr int S = 32 / (int)sizeof(T);  // a ring slot of x and g: 4 KiB per warp
-  static constexpr int kTile = S * kGrWarps;
-  static constexpr int kSlot = 2 * S * kGrCols;  // elements
+  static constexpr int kTile = S * G * kGrWarps;
+  static constexpr int kSlot = 2 * S * 64;  // elements
   static constexpr size_t kSmem = sizeof(GrShared) + sizeof(T) * kGrWarps * kGrStages * kSlot;
   static_assert(kGrChunk % S == 0 && kTile % kGrChunk == 0, "chunks start with a warp's tokens");
 };
 
 // The number of rounds goes by L alone, never by what memory holds: every thread
 // of a cluster reaches the same barriers.
-template <typename T, int CW>
+template <typename T, int G, int CW>
 __global__ void __launch_bounds__(kGrThreads, 2) gatedrec_fwd_kernel(const GrFwdParams p) {
-  using Shape = GrFwdShape<T>;
-  constexpr int S = Shape::S, kTile = Shape::kTile;
+  using Shape = GrFwdShape<T, G>;
+  constexpr int S = Shape::S, kTile = Shape::kTile, kCols = 64 / G;
   constexpr bool kPair = CW > (int)sizeof(T);
   extern __shared__ __align__(16) unsigned char gr_smem[];
   GrShared& sh = *reinterpret_cast<GrShared*>(gr_smem);
-  gr_cluster_begin(sh, p.N);
+  gr_cluster_begin<G>(sh, p.N);
   umma::grid_dep_wait();
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int grp = lane / (32 / G), pair = lane % (32 / G) * 2;
   T* ring = reinterpret_cast<T*>(gr_smem + sizeof(GrShared)) + w * kGrStages * Shape::kSlot;
   const int rank = blockIdx.x % p.N, cid = blockIdx.x / p.N;
-  const int b = cid / p.n_blk, c0 = cid % p.n_blk * kGrCols, c = c0 + 2 * lane;
+  const int b = cid / p.n_blk, c0 = cid % p.n_blk * kCols, c = c0 + pair;
   const int len = gr_length(p.lengths, b, p.L), end = max(len, 0);
   const bool live = c < p.D && len >= 0, two = c + 1 < p.D;
-  const int cols = min(p.D - c0, kGrCols);
+  const int cols = min(p.D - c0, kCols);
   const T* x = static_cast<const T*>(p.x) + (size_t)b * p.L * p.D + c0;
   const T* g = static_cast<const T*>(p.g) + (size_t)b * p.L * p.D + c0;
-  T* y = static_cast<T*>(p.y) + (size_t)b * p.L * p.D + c;
+  T* y = static_cast<T*>(p.y) + (size_t)b * p.L * p.D;
   const int n_chunks = (p.L + kGrChunk - 1) / kGrChunk;
 
   F2 h = f2(0.0f, 0.0f);
@@ -256,9 +303,9 @@ __global__ void __launch_bounds__(kGrThreads, 2) gatedrec_fwd_kernel(const GrFwd
   auto fetch = [&](int k) {
     if (k < rounds) {
       T* slot = ring + k % kGrStages * Shape::kSlot;
-      const int t0 = (k * p.N + rank) * kTile + w * S;
-      gr_fetch<T, S, CW>(slot, x, p.D, t0, end, cols, lane);
-      gr_fetch<T, S, CW>(slot + S * kGrCols, g, p.D, t0, end, cols, lane);
+      const int t0 = (k * p.N + rank) * kTile + w * G * S;
+      gr_fetch<T, S, G, CW>(slot, x, p.D, t0, end, cols, lane);
+      gr_fetch<T, S, G, CW>(slot + S * 64, g, p.D, t0, end, cols, lane);
     }
     umma::cp_async_commit();
   };
@@ -266,19 +313,19 @@ __global__ void __launch_bounds__(kGrThreads, 2) gatedrec_fwd_kernel(const GrFwd
   for (int k = 0; k < kGrStages - 1; ++k) fetch(k);
   bool ok = true;
   for (int k = 0; k < rounds; ++k) {
-    const int t0 = (k * p.N + rank) * kTile + w * S;
+    const int t0 = (k * p.N + rank) * kTile + (w * G + grp) * S;  // this lane's first token
     umma::cp_async_wait<kGrStages - 2>();
     __syncwarp();
     fetch(k + kGrStages - 1);  // into the slot read in the round before
-    const T* xs = ring + k % kGrStages * Shape::kSlot + 2 * lane;
-    const T* gs = xs + S * kGrCols;
+    const T* xs = ring + k % kGrStages * Shape::kSlot + grp * kCols + pair;
+    const T* gs = xs + S * 64;
     F2 a[S], u[S];  // h -> a h + u
     GrMap m = map_one();
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      const Gate2 gt = gate_of(load_pair(gs + s * kGrCols));
+      const Gate2 gt = gate_of(load_pair(gs + s * 64));
       a[s] = gt.a;
-      u[s] = gt.n * load_pair(xs + s * kGrCols);
+      u[s] = gt.n * load_pair(xs + s * 64);
     }
     if (t0 + S > end) {  // past the end: the identity
 #pragma unroll
@@ -291,30 +338,32 @@ __global__ void __launch_bounds__(kGrThreads, 2) gatedrec_fwd_kernel(const GrFwd
 #pragma unroll
     for (int s = 0; s < S; ++s) map_then(m, GrMap{a[s], u[s]});
     F2 e;
-    ok = gr_round(sh, k, w, rank, p.N, lane, m, h, e, ok, [](int r) { return r; });
+    ok = gr_round<G, false>(sh, k, w, rank, grp, p.N, lane, m, h, e, ok, [](int r) { return r; });
     if (live) {
       if (p.h_chunks && t0 % kGrChunk == 0 && t0 < p.L)
         gr_store<kPair>(p.h_chunks + ((size_t)b * n_chunks + t0 / kGrChunk) * p.D + c,
                         t0 < end ? e : f2(0.0f, 0.0f), two);
-      T* out = y + (size_t)t0 * p.D;
+      // the tile's outputs at 32-bit offsets from its first token
+      T* out = y + (size_t)(k * p.N + rank) * kTile * p.D;
+      uint32_t at = (uint32_t)((w * G + grp) * S) * p.D + c;
       if (t0 + S <= end) {
 #pragma unroll
-        for (int s = 0; s < S; ++s, out += p.D) {
+        for (int s = 0; s < S; ++s, at += p.D) {
           e = f2_fma(a[s], e, u[s]);
-          gr_store<kPair>(out, e, two);
+          gr_store<kPair>(out + at, e, two);
         }
       } else {
 #pragma unroll
-        for (int s = 0; s < S; ++s, out += p.D) {
+        for (int s = 0; s < S; ++s, at += p.D) {
           e = f2_fma(a[s], e, u[s]);
-          if (t0 + s < p.L) gr_store<kPair>(out, t0 + s < end ? e : f2(0.0f, 0.0f), two);
+          if (t0 + s < p.L) gr_store<kPair>(out + at, t0 + s < end ? e : f2(0.0f, 0.0f), two);
         }
       }
     }
   }
   gr_cluster_end(p.N, ok);
   if (p.h_last) {
-    if (live && rank == 0 && w == 0) gr_store<kPair>(p.h_last + (size_t)b * p.D + c, h, two);
+    if (live && rank == 0 && w == 0 && grp == 0) gr_store<kPair>(p.h_last + (size_t)b * p.D + c, h, two);
   }
 }
 
@@ -326,11 +375,12 @@ struct GrBwdParams {
   int L, D, n_blk, N;
 };
 
-template <typename T>
+template <typename T, int G>
 struct GrBwdShape {
-  // tiles of one chunk: the forward states of a tile start from its saved state
-  static constexpr int S = kGrChunk / kGrWarps;
-  static constexpr int kSlot = 3 * S * kGrCols;
+  static constexpr int S = 8;
+  static constexpr int kTile = S * G * kGrWarps;
+  static constexpr int kSlot = 3 * S * 64;
+  static_assert(kTile % kGrChunk == 0, "the forward states of a tile start from a saved state");
   static constexpr size_t kShared = sizeof(GrShared) + sizeof(ulonglong2) * 2 * kGrWarps * 32;
   static constexpr size_t kSmem = kShared + sizeof(T) * kGrWarps * kGrStages * kSlot;
 };
@@ -338,23 +388,24 @@ struct GrBwdShape {
 // The same cut, walked from the end.  The state that enters a tile is the saved
 // one, so the forward maps only have to meet inside the CTA; the gradient's maps
 // l -> A l + Q go through the cluster.
-template <typename T, int CW>
+template <typename T, int G, int CW>
 __global__ void __launch_bounds__(kGrThreads, 2) gatedrec_bwd_kernel(const GrBwdParams p) {
-  using Shape = GrBwdShape<T>;
-  constexpr int S = Shape::S, kTile = kGrChunk;
+  using Shape = GrBwdShape<T, G>;
+  constexpr int S = Shape::S, kTile = Shape::kTile, kCols = 64 / G;
   constexpr bool kPair = CW > (int)sizeof(T);
   extern __shared__ __align__(16) unsigned char gr_smem[];
   GrShared& sh = *reinterpret_cast<GrShared*>(gr_smem);
   auto fwd = reinterpret_cast<ulonglong2(*)[kGrWarps][32]>(gr_smem + sizeof(GrShared));
-  gr_cluster_begin(sh, p.N);
+  gr_cluster_begin<G>(sh, p.N);
   umma::grid_dep_wait();
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int grp = lane / (32 / G), pair = lane % (32 / G) * 2;
   T* ring = reinterpret_cast<T*>(gr_smem + Shape::kShared) + w * kGrStages * Shape::kSlot;
   const int rank = blockIdx.x % p.N, cid = blockIdx.x / p.N;
-  const int b = cid / p.n_blk, c0 = cid % p.n_blk * kGrCols, c = c0 + 2 * lane;
+  const int b = cid / p.n_blk, c0 = cid % p.n_blk * kCols, c = c0 + pair;
   const int len = gr_length(p.lengths, b, p.L), end = max(len, 0);
   const bool live = c < p.D && len >= 0, two = c + 1 < p.D;
-  const int cols = min(p.D - c0, kGrCols);
+  const int cols = min(p.D - c0, kCols);
   const size_t seq = (size_t)b * p.L * p.D;
   const T* x = static_cast<const T*>(p.x) + seq + c0;
   const T* g = static_cast<const T*>(p.g) + seq + c0;
@@ -370,10 +421,10 @@ __global__ void __launch_bounds__(kGrThreads, 2) gatedrec_bwd_kernel(const GrBwd
   auto fetch = [&](int k) {
     if (k < rounds) {
       T* slot = ring + k % kGrStages * Shape::kSlot;
-      const int t0 = first(k) + w * S;
-      gr_fetch<T, S, CW>(slot, x, p.D, t0, end, cols, lane);
-      gr_fetch<T, S, CW>(slot + S * kGrCols, g, p.D, t0, end, cols, lane);
-      gr_fetch<T, S, CW>(slot + 2 * S * kGrCols, dy, p.D, t0, end, cols, lane);
+      const int t0 = first(k) + w * G * S;
+      gr_fetch<T, S, G, CW>(slot, x, p.D, t0, end, cols, lane);
+      gr_fetch<T, S, G, CW>(slot + S * 64, g, p.D, t0, end, cols, lane);
+      gr_fetch<T, S, G, CW>(slot + 2 * S * 64, dy, p.D, t0, end, cols, lane);
     }
     umma::cp_async_commit();
   };
@@ -386,21 +437,21 @@ __global__ void __launch_bounds__(kGrThreads, 2) gatedrec_bwd_kernel(const GrBwd
   bool ok = true;
   F2 next = saved(0);
   for (int k = 0; k < rounds; ++k) {
-    const int t0 = first(k) + w * S;
+    const int t0 = first(k) + (w * G + grp) * S;  // this lane's first token
     F2 h = next;  // the state that enters the tile
     next = saved(k + 1);
     umma::cp_async_wait<kGrStages - 2>();
     __syncwarp();
     fetch(k + kGrStages - 1);
-    const T* xs = ring + k % kGrStages * Shape::kSlot + 2 * lane;
+    const T* xs = ring + k % kGrStages * Shape::kSlot + grp * kCols + pair;
     F2 a[S], n[S], xv[S], d[S];
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      const Gate2 gt = gate_of(load_pair(xs + (S + s) * kGrCols));
+      const Gate2 gt = gate_of(load_pair(xs + (S + s) * 64));
       a[s] = gt.a;
       n[s] = gt.n;
-      xv[s] = load_pair(xs + s * kGrCols);
-      d[s] = load_pair(xs + (2 * S + s) * kGrCols);
+      xv[s] = load_pair(xs + s * 64);
+      d[s] = load_pair(xs + (2 * S + s) * 64);
     }
     if (t0 + S > end) {  // past the end: the identity (x and dy were copied as zero)
 #pragma unroll
@@ -417,36 +468,38 @@ __global__ void __launch_bounds__(kGrThreads, 2) gatedrec_bwd_kernel(const GrBwd
     q.H = zero;
 #pragma unroll
     for (int s = S - 1; s >= 0; --s) q.H = a[s] * (q.H + d[s]);
-    map_store(&fwd[k & 1][w][lane], f);
+    const GrMap groups = map_scan_groups<G, false>(f, grp, lane);
+    if (grp == G - 1) map_store(&fwd[k & 1][w][pair / 2], f);
     // the scan runs from the last token: positions count from the end
     F2 e;
-    ok = gr_round(sh, k, kGrWarps - 1 - w, p.N - 1 - rank, p.N, lane, q, l, e, ok,
-                  [&](int r) { return p.N - 1 - r; });
+    ok = gr_round<G, true>(sh, k, kGrWarps - 1 - w, p.N - 1 - rank, G - 1 - grp, p.N, lane, q, l,
+                           e, ok, [&](int r) { return p.N - 1 - r; });
     if (live) {
-      for (int i = 0; i < w; ++i) map_apply(h, map_load(&fwd[k & 1][i][lane]));
+      for (int i = 0; i < w; ++i) map_apply(h, map_load(&fwd[k & 1][i][pair / 2]));
+      map_apply(h, groups);
 #pragma unroll
       for (int s = 0; s < S; ++s) {
         const F2 u = n[s] * xv[s];
         xv[s] = f2_fma(xv[s], minus, h);  // h_{t-1} - x_t
         h = f2_fma(a[s], h, u);
       }
-      const size_t at = seq + (size_t)t0 * p.D + c;
-      float *dx = p.dx + at, *dg = p.dg + at;
+        float *dx = p.dx + seq + (size_t)first(k) * p.D, *dg = p.dg + seq + (size_t)first(k) * p.D;
+      uint32_t at = (uint32_t)((w * G + grp) * S + S - 1) * p.D + c;
 #pragma unroll
-      for (int s = S - 1; s >= 0; --s) {
+      for (int s = S - 1; s >= 0; --s, at -= p.D) {
         const F2 lt = e + d[s];
         const F2 dxv = n[s] * lt;  // past the end n is 0
         e = a[s] * lt;
         if (t0 + s < p.L) {
-          gr_store<kPair>(dx + (size_t)s * p.D, dxv, two);
-          gr_store<kPair>(dg + (size_t)s * p.D, dxv * xv[s] * a[s], two);
+          gr_store<kPair>(dx + at, dxv, two);
+          gr_store<kPair>(dg + at, dxv * xv[s] * a[s], two);
         }
       }
     }
   }
   gr_cluster_end(p.N, ok);
   if (p.dh0) {
-    if (live && rank == 0 && w == 0) gr_store<kPair>(p.dh0 + (size_t)b * p.D + c, l, two);
+    if (live && rank == 0 && w == 0 && grp == 0) gr_store<kPair>(p.dh0 + (size_t)b * p.D + c, l, two);
   }
 }
 

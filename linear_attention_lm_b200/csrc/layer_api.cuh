@@ -185,7 +185,8 @@ based_status_t check_gatedrec(const void* x, const void* g, const void* y, const
   for (const void* t : {x, g, y})
     if ((s = check_tensor(t, empty)) != BASED_OK) return s;
   if (reinterpret_cast<uintptr_t>(lengths) & 7u) return BASED_ERR_INVALID_ARG;
-  if ((long long)B * ceil_div(D, 32) > 0x7fffffffLL || L > 0x7fff0000) return BASED_ERR_UNSUPPORTED;
+  if ((long long)B * ceil_div(D, 16) > 0x7fffffffLL || L > 0x7fff0000 || D > kGrMaxD)
+    return BASED_ERR_UNSUPPORTED;
   return BASED_OK;
 }
 
@@ -221,14 +222,31 @@ bool launch_gatedrec(void (*kern)(P), const P& p, long long clusters, size_t sme
   return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess;
 }
 
-// CTAs per cluster: as many as fit on the GPU at once at two CTAs per SM, and no
-// more than there are tiles.
-inline int gatedrec_cluster(long long clusters, int L, int tile) {
-  int N = 1;
-  while (2 * N <= kGrMaxCluster && clusters * 2 * N <= 2LL * device_sm_count() &&
-         (long long)N * tile < L)
-    N *= 2;
-  return N;
+// The cut of a recurrence: G groups of lanes per warp (64 / G channels per CTA) and N
+// CTAs per cluster, for up to two CTAs per SM.  Two groups cost less than two CTAs
+// (8 x 2048 x 1024 bf16: forward 24.2 us with G = 2, N = 1, 27.6 with G = 1, N = 2 and
+// 28.1 with neither; gradient 46.7, 58.1 and 54.4), but rows of 32 bytes (G = 4) lose
+// to eight CTAs (1 x 16384 x 1024: forward 31.4 us with G = 2, N = 8, 33.5 with G = 4,
+// N = 4), so G = 4 is for fewer channels than eight CTAs fill the GPU with.
+struct GrPlan {
+  int G, N, n_blk;
+};
+inline GrPlan plan_gatedrec(int B, int L, int D, int group_tokens) {
+  const long long slots = 2LL * device_sm_count();
+  auto cut = [&](int G) {
+    GrPlan pl{G, 1, (int)ceil_div(D, 64 / G)};
+    const long long clusters = (long long)B * pl.n_blk, tile = (long long)G * kGrWarps * group_tokens;
+    while (pl.N < kGrMaxCluster && clusters * (pl.N + 1) <= slots && pl.N * tile < L) ++pl.N;
+    return pl;
+  };
+  // more groups while they double the CTAs at work and each still has tokens
+  auto more = [&](int G) {
+    return B * ceil_div(D, 64 / G) <= slots && (long long)G / 2 * kGrWarps * group_tokens < L;
+  };
+  GrPlan pl = cut(1);
+  if (more(2)) pl = cut(2);
+  if (pl.G == 2 && more(4) && (long long)B * pl.n_blk * pl.N * 2 <= slots) pl = cut(4);
+  return pl;
 }
 
 }  // namespace
@@ -349,17 +367,22 @@ based_status_t based_gatedrec_fwd(const void* x, const void* g, void* y, const f
   if (s != BASED_OK) return s;
   if (!aligned16(h0) || !aligned16(h_last) || !aligned16(h_chunks)) return BASED_ERR_INVALID_ARG;
   if (B == 0 || (L == 0 && !h_last)) return BASED_OK;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
   GrFwdParams p{};
   p.x = x; p.g = g; p.y = y; p.h0 = h0; p.h_last = h_last; p.h_chunks = h_chunks;
   p.lengths = lengths; p.L = L; p.D = D;
   return for_copies(dt, D, [&](auto t, auto cw) -> based_status_t {
     using T = decltype(t);
-    p.n_blk = (int)ceil_div(D, kGrCols);
-    const long long clusters = (long long)B * p.n_blk;
-    p.N = gatedrec_cluster(clusters, L, GrFwdShape<T>::kTile);
-    if (!launch_gatedrec(gatedrec_fwd_kernel<T, decltype(cw)::value>, p, clusters,
-                         GrFwdShape<T>::kSmem, static_cast<cudaStream_t>(stream)))
-      return BASED_ERR_CUDA;
+    constexpr int CW = decltype(cw)::value;
+    const GrPlan pl = plan_gatedrec(B, L, D, GrFwdShape<T, 1>::S);
+    p.n_blk = pl.n_blk;
+    p.N = pl.N;
+    const long long clusters = (long long)B * pl.n_blk;
+    const size_t smem = GrFwdShape<T, 1>::kSmem;  // the same for every G
+    const bool ok = pl.G == 1   ? launch_gatedrec(gatedrec_fwd_kernel<T, 1, CW>, p, clusters, smem, st)
+                    : pl.G == 2 ? launch_gatedrec(gatedrec_fwd_kernel<T, 2, CW>, p, clusters, smem, st)
+                                : launch_gatedrec(gatedrec_fwd_kernel<T, 4, CW>, p, clusters, smem, st);
+    if (!ok) return BASED_ERR_CUDA;
     return launch_status();
   });
 }
@@ -376,17 +399,22 @@ based_status_t based_gatedrec_bwd(const void* x, const void* g, const void* dy,
     if ((s = check_tensor(t, empty)) != BASED_OK) return s;
   if (!aligned16(dh_last) || !aligned16(dh0)) return BASED_ERR_INVALID_ARG;
   if (B == 0 || (L == 0 && !dh0)) return BASED_OK;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
   GrBwdParams p{};
   p.x = x; p.g = g; p.dy = dy; p.h_chunks = h_chunks; p.dh_last = dh_last;
   p.dx = dx; p.dg = dg; p.dh0 = dh0; p.lengths = lengths; p.L = L; p.D = D;
   return for_copies(dt, D, [&](auto t, auto cw) -> based_status_t {
     using T = decltype(t);
-    p.n_blk = (int)ceil_div(D, kGrCols);
-    const long long clusters = (long long)B * p.n_blk;
-    p.N = gatedrec_cluster(clusters, L, kGrChunk);
-    if (!launch_gatedrec(gatedrec_bwd_kernel<T, decltype(cw)::value>, p, clusters,
-                         GrBwdShape<T>::kSmem, static_cast<cudaStream_t>(stream)))
-      return BASED_ERR_CUDA;
+    constexpr int CW = decltype(cw)::value;
+    const GrPlan pl = plan_gatedrec(B, L, D, GrBwdShape<T, 1>::S);
+    p.n_blk = pl.n_blk;
+    p.N = pl.N;
+    const long long clusters = (long long)B * pl.n_blk;
+    const size_t smem = GrBwdShape<T, 1>::kSmem;  // the same for every G
+    const bool ok = pl.G == 1   ? launch_gatedrec(gatedrec_bwd_kernel<T, 1, CW>, p, clusters, smem, st)
+                    : pl.G == 2 ? launch_gatedrec(gatedrec_bwd_kernel<T, 2, CW>, p, clusters, smem, st)
+                                : launch_gatedrec(gatedrec_bwd_kernel<T, 4, CW>, p, clusters, smem, st);
+    if (!ok) return BASED_ERR_CUDA;
     return launch_status();
   });
 }

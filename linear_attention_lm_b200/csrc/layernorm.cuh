@@ -164,7 +164,7 @@ struct LnBwdShape {
   static size_t smem(int tpr, int D) {
     const size_t ring = kAsync ? (size_t)kStages * kThread * kThreads : 0;
     const size_t join = tpr < kThreads ? (size_t)D * 8 : 0;
-    return ring > join ? ring : join;
+    return join > ring ? join : ring;
   }
 };
 
