@@ -490,12 +490,10 @@ def based_baseconv_fwd(x, w, bias, taps, y, stream=None):
     return y
 
 
-def _arg(t, shape, dtype, name: str, device: torch.device):
+def _need(t, shape, dtype, name: str, device: torch.device, index: int):
     """Pointer of a tensor that must have exactly this shape and dtype, be
-    contiguous and sit on this device (None stays None)."""
-    if t is None:
-        return None
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device.index
+    contiguous and sit on this device (index: the device's)."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
             and t.shape == shape and t.is_contiguous()):
         return t.data_ptr() or None
     if not isinstance(t, torch.Tensor):
@@ -507,6 +505,11 @@ def _arg(t, shape, dtype, name: str, device: torch.device):
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     raise ValueError(f"{name} must be contiguous")
+
+
+def _may(t, shape, dtype, name: str, device: torch.device, index: int):
+    """The same for a tensor that may be left out (None)."""
+    return None if t is None else _need(t, shape, dtype, name, device, index)
 
 
 # the current stream's handle without a stream object around it
@@ -535,32 +538,26 @@ def _run(fn: str, args, stream, device: torch.device):
         raise BasedError(fn, st)
 
 
-def _required(**ts):
-    for name, t in ts.items():
-        if t is None:
-            raise TypeError(f"{name}: expected a torch.Tensor")
-
-
 def based_layernorm_fwd(x, weight, bias, y, eps: float = 1e-5, residual=None, resid_out=None,
                         mean=None, rstd=None, stream=None):
     """y = layer norm of r = x (+ residual) over the last axis, times weight
     (+ bias).  x, y, residual, resid_out [..., D]; weight, bias [D] float32; mean,
     rstd float32 of x's leading shape (written if given, for the gradient)."""
-    _required(x=x, weight=weight, y=y)
     dev = _cuda(_device_of(x))
     if x.dim() < 1:
         raise ValueError("x must be [..., D]")
-    shape, dtype = x.shape, x.dtype
+    shape, dtype, f32, at = x.shape, x.dtype, torch.float32, dev.index
     dt = _dtype_code(x)
-    lead, D = shape[:-1], shape[-1]
+    lead, row = shape[:-1], shape[-1:]
     if (residual is None) != (resid_out is None):
         raise ValueError("residual and resid_out are given together")
-    f32 = torch.float32
-    args = (_arg(x, shape, dtype, "x", dev), _arg(residual, shape, dtype, "residual", dev),
-            _arg(weight, (D,), f32, "weight", dev), _arg(bias, (D,), f32, "bias", dev),
-            _arg(y, shape, dtype, "y", dev), _arg(resid_out, shape, dtype, "resid_out", dev),
-            _arg(mean, lead, f32, "mean", dev), _arg(rstd, lead, f32, "rstd", dev))
-    _run("based_layernorm_fwd", (*args, lead.numel(), D, dt, float(eps)), stream, dev)
+    args = (_need(x, shape, dtype, "x", dev, at), _may(residual, shape, dtype, "residual", dev, at),
+            _need(weight, row, f32, "weight", dev, at), _may(bias, row, f32, "bias", dev, at),
+            _need(y, shape, dtype, "y", dev, at),
+            _may(resid_out, shape, dtype, "resid_out", dev, at),
+            _may(mean, lead, f32, "mean", dev, at), _may(rstd, lead, f32, "rstd", dev, at),
+            lead.numel(), row[0], dt, eps)
+    _run("based_layernorm_fwd", args, stream, dev)
     return y
 
 
@@ -576,20 +573,18 @@ def based_layernorm_bwd(dy, x, weight, mean, rstd, dx, dweight, dbias, dresid=No
     """Gradients (float32, written) of based_layernorm_fwd: dx [..., D] (with
     dresid added, the gradient that reaches the residual stream from elsewhere),
     dweight, dbias [D].  x is the normalised stream (resid_out, or x)."""
-    _required(dy=dy, x=x, weight=weight, mean=mean, rstd=rstd, dx=dx, dweight=dweight)
     dev = _cuda(_device_of(x))
     if x.dim() < 1:
         raise ValueError("x must be [..., D]")
-    shape, dtype = x.shape, x.dtype
+    shape, dtype, f32, at = x.shape, x.dtype, torch.float32, dev.index
     dt = _dtype_code(x)
-    lead, D = shape[:-1], shape[-1]
-    rows = lead.numel()
-    f32 = torch.float32
-    args = (_arg(dy, shape, dtype, "dy", dev), _arg(x, shape, dtype, "x", dev),
-            _arg(weight, (D,), f32, "weight", dev), _arg(mean, lead, f32, "mean", dev),
-            _arg(rstd, lead, f32, "rstd", dev), _arg(dresid, shape, f32, "dresid", dev),
-            _arg(dx, shape, f32, "dx", dev), _arg(dweight, (D,), f32, "dweight", dev),
-            _arg(dbias, (D,), f32, "dbias", dev))
+    lead, row = shape[:-1], shape[-1:]
+    rows, D = lead.numel(), row[0]
+    args = (_need(dy, shape, dtype, "dy", dev, at), _need(x, shape, dtype, "x", dev, at),
+            _need(weight, row, f32, "weight", dev, at), _need(mean, lead, f32, "mean", dev, at),
+            _need(rstd, lead, f32, "rstd", dev, at), _may(dresid, shape, f32, "dresid", dev, at),
+            _need(dx, shape, f32, "dx", dev, at), _need(dweight, row, f32, "dweight", dev, at),
+            _may(dbias, row, f32, "dbias", dev, at))
     if workspace is None:
         stream = _torch_stream(stream, dev)
         with torch.cuda.device(dev):
@@ -619,6 +614,12 @@ def based_rotary_freqs(rot_dim: int, base: float = 10000.0, scaling: str = "none
     return freqs
 
 
+def _shape_of(t, name: str):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    return t.shape
+
+
 def _rotary(fn, q, k, q_out, k_out, freqs, pos, layout, mscale, dtype, stream):
     ref = q if q is not None else k
     dev = _cuda(_device_of(ref))
@@ -628,24 +629,23 @@ def _rotary(fn, q, k, q_out, k_out, freqs, pos, layout, mscale, dtype, stream):
         raise ValueError("q, k must be [B, H, L, d_head]")
     if layout not in ROTARY_LAYOUTS:
         raise ValueError(f"layout: one of {sorted(ROTARY_LAYOUTS)}, got {layout!r}")
-    B, _, L, D = ref.shape
-    if k is not None and k is not ref and (k.dim() != 4 or k.shape[0] != B or
-                                           k.shape[2:] != ref.shape[2:]):
-        raise ValueError(f"k: expected shape {(B, 'H', L, D)}, got {tuple(k.shape)}")
+    shape = ref.shape
+    B, _, L, D = shape
+    k_shape = None if k is None else _shape_of(k, "k")
+    if k_shape is not None and (len(k_shape) != 4 or k_shape[0] != B or k_shape[2:] != shape[2:]):
+        raise ValueError(f"k: expected shape {(B, 'H', L, D)}, got {tuple(k_shape)}")
     dtype = dtype or ref.dtype
     dt = _dtype_code(ref)
     if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
         raise TypeError("freqs must be a float64 tensor [rot_dim / 2]")
+    f_shape, at = freqs.shape, dev.index
     per_seq = isinstance(pos, torch.Tensor)
-    H_q, H_k = q.shape[1] if q is not None else 0, k.shape[1] if k is not None else 0
-    args = (_arg(q, ref.shape, dtype, "q", dev), _arg(k, k.shape if k is not None else None,
-                                                      dtype, "k", dev),
-            _arg(q_out, ref.shape, dtype, "q_out", dev),
-            _arg(k_out, k.shape if k is not None else None, dtype, "k_out", dev),
-            _arg(freqs, freqs.shape, torch.float64, "freqs", dev),
-            _arg(pos, (B,), torch.int64, "pos", dev) if per_seq else None,
-            0 if per_seq else int(pos), B, H_q, H_k, L, D, 2 * freqs.shape[0],
-            ROTARY_LAYOUTS[layout], float(mscale))
+    args = (_may(q, shape, dtype, "q", dev, at), _may(k, k_shape, dtype, "k", dev, at),
+            _may(q_out, shape, dtype, "q_out", dev, at), _may(k_out, k_shape, dtype, "k_out", dev, at),
+            _need(freqs, f_shape, torch.float64, "freqs", dev, at),
+            _need(pos, (B,), torch.int64, "pos", dev, at) if per_seq else None,
+            0 if per_seq else int(pos), B, 0 if q is None else shape[1],
+            0 if k is None else k_shape[1], L, D, 2 * f_shape[0], ROTARY_LAYOUTS[layout], mscale)
     if per_seq and B == 0:
         return q_out, k_out
     _run(fn, (*args, dt) if fn == "based_rotary_fwd" else args, stream, dev)
@@ -675,24 +675,25 @@ GATEDREC_CHUNK = 64
 
 def _gatedrec_args(x):
     dev = _cuda(_device_of(x))
-    if x.dim() != 3:
+    shape = x.shape
+    if len(shape) != 3:
         raise ValueError("x, g must be [B, L, D]")
-    B, L, D = x.shape
-    return dev, B, L, D, (B, -(-L // GATEDREC_CHUNK), D), _dtype_code(x)
+    B, L, D = shape
+    return dev, dev.index, shape, x.dtype, (B, D), (B, -(-L // GATEDREC_CHUNK), D), _dtype_code(x)
 
 
 def based_gatedrec_fwd(x, g, y, h0=None, h_last=None, h_chunks=None, lengths=None, stream=None):
     """y_t = h_t = a_t h_{t-1} + (1 - a_t) x_t, a = sigmoid(g): x, g, y [B, L, D];
     h0, h_last [B, D] float32; h_chunks [B, ceil(L / 64), D] float32 (written, for
     the gradient); lengths int64 CUDA tensor [B]."""
-    _required(x=x, g=g, y=y)
-    dev, B, L, D, chunks, dt = _gatedrec_args(x)
+    dev, at, shape, dtype, state, chunks, dt = _gatedrec_args(x)
     f32 = torch.float32
-    args = (_arg(x, x.shape, x.dtype, "x", dev), _arg(g, x.shape, x.dtype, "g", dev),
-            _arg(y, x.shape, x.dtype, "y", dev), _arg(h0, (B, D), f32, "h0", dev),
-            _arg(h_last, (B, D), f32, "h_last", dev), _arg(h_chunks, chunks, f32, "h_chunks", dev),
-            _arg(lengths, (B,), torch.int64, "lengths", dev))
-    _run("based_gatedrec_fwd", (*args, B, L, D, dt), stream, dev)
+    _run("based_gatedrec_fwd",
+         (_need(x, shape, dtype, "x", dev, at), _need(g, shape, dtype, "g", dev, at),
+          _need(y, shape, dtype, "y", dev, at), _may(h0, state, f32, "h0", dev, at),
+          _may(h_last, state, f32, "h_last", dev, at),
+          _may(h_chunks, chunks, f32, "h_chunks", dev, at),
+          _may(lengths, shape[:1], torch.int64, "lengths", dev, at), *shape, dt), stream, dev)
     return y
 
 
@@ -700,29 +701,27 @@ def based_gatedrec_bwd(x, g, dy, h_chunks, dx, dg, dh_last=None, dh0=None, lengt
                        stream=None):
     """Gradients (float32, written) of based_gatedrec_fwd given dy and, if the
     final state was used, dh_last; h_chunks is what the forward wrote."""
-    _required(x=x, g=g, dy=dy, h_chunks=h_chunks, dx=dx, dg=dg)
-    dev, B, L, D, chunks, dt = _gatedrec_args(x)
+    dev, at, shape, dtype, state, chunks, dt = _gatedrec_args(x)
     f32 = torch.float32
-    args = (_arg(x, x.shape, x.dtype, "x", dev), _arg(g, x.shape, x.dtype, "g", dev),
-            _arg(dy, x.shape, x.dtype, "dy", dev), _arg(h_chunks, chunks, f32, "h_chunks", dev),
-            _arg(dh_last, (B, D), f32, "dh_last", dev), _arg(dx, x.shape, f32, "dx", dev),
-            _arg(dg, x.shape, f32, "dg", dev), _arg(dh0, (B, D), f32, "dh0", dev),
-            _arg(lengths, (B,), torch.int64, "lengths", dev))
-    _run("based_gatedrec_bwd", (*args, B, L, D, dt), stream, dev)
+    _run("based_gatedrec_bwd",
+         (_need(x, shape, dtype, "x", dev, at), _need(g, shape, dtype, "g", dev, at),
+          _need(dy, shape, dtype, "dy", dev, at), _need(h_chunks, chunks, f32, "h_chunks", dev, at),
+          _may(dh_last, state, f32, "dh_last", dev, at), _need(dx, shape, f32, "dx", dev, at),
+          _need(dg, shape, f32, "dg", dev, at), _may(dh0, state, f32, "dh0", dev, at),
+          _may(lengths, shape[:1], torch.int64, "lengths", dev, at), *shape, dt), stream, dev)
     return dx, dg, dh0
 
 
 def based_gatedrec_step(x, g, h, y, stream=None):
     """One token: h [B, D] float32 becomes a h + (1 - a) x (in place), y [B, D] = h."""
-    _required(x=x, g=g, h=h, y=y)
     dev = _cuda(_device_of(x))
-    if x.dim() != 2:
+    shape, dtype, at = x.shape, x.dtype, dev.index
+    if len(shape) != 2:
         raise ValueError("x, g must be [B, D]")
-    B, D = x.shape
-    dt = _dtype_code(x)
-    args = (_arg(x, x.shape, x.dtype, "x", dev), _arg(g, x.shape, x.dtype, "g", dev),
-            _arg(h, x.shape, torch.float32, "h", dev), _arg(y, x.shape, x.dtype, "y", dev))
-    _run("based_gatedrec_step", (*args, B, D, dt), stream, dev)
+    _run("based_gatedrec_step",
+         (_need(x, shape, dtype, "x", dev, at), _need(g, shape, dtype, "g", dev, at),
+          _need(h, shape, torch.float32, "h", dev, at), _need(y, shape, dtype, "y", dev, at),
+          *shape, _dtype_code(x)), stream, dev)
     return y
 
 
