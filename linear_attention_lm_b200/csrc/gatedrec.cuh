@@ -120,7 +120,8 @@ struct GrShared {
   ulonglong2 warp[2][kGrWarps][32];
   ulonglong2 cta[2][kGrMaxCluster][32];
   uint64_t bar[2];
-  uint64_t pad[6];
+  int len;
+  int pad[11];
 };
 template <int G>
 __device__ __forceinline__ uint32_t gr_round_bytes(int N) {
@@ -231,15 +232,18 @@ __device__ __forceinline__ void gr_fetch(T* slot, const T* src, int D, int t0, i
   }
 }
 
-// Length of sequence b; -1 (and a recorded error) if the array's entry is not in [0, L].
-__device__ __forceinline__ int gr_length(const long long* lengths, int b, int L) {
+// Length of sequence b; -1 (and a recorded error) if the array's entry is not in
+// [0, L].  One thread reads it for the CTA, whose barriers then agree.
+__device__ __forceinline__ int gr_length(GrShared& sh, const long long* lengths, int b, int L) {
   if (!lengths) return L;
-  const long long n = lengths[b];
-  if (n < 0 || n > L) {
-    record_device_error(BASED_ERR_INVALID_ARG);
-    return -1;
+  if (threadIdx.x == 0) {
+    const long long n = lengths[b];
+    const bool in = n >= 0 && n <= L;
+    if (!in) record_device_error(BASED_ERR_INVALID_ARG);
+    sh.len = in ? (int)n : -1;
   }
-  return (int)n;
+  __syncthreads();
+  return sh.len;
 }
 
 // Two channels of an fp32 [.., D] row at p; kPair: rows start at even elements.
@@ -272,8 +276,8 @@ struct GrFwdShape {
   static_assert(kGrChunk % S == 0 && kTile % kGrChunk == 0, "chunks start with a warp's tokens");
 };
 
-// The number of rounds goes by L alone, never by what memory holds: every thread
-// of a cluster reaches the same barriers.
+// Rounds that lie past the end of a sequence are not walked: their outputs are
+// zeros, written at the end.
 template <typename T, int G, int CW>
 __global__ void __launch_bounds__(kGrThreads, 2) gatedrec_fwd_kernel(const GrFwdParams p) {
   using Shape = GrFwdShape<T, G>;
@@ -288,7 +292,7 @@ __global__ void __launch_bounds__(kGrThreads, 2) gatedrec_fwd_kernel(const GrFwd
   T* ring = reinterpret_cast<T*>(gr_smem + sizeof(GrShared)) + w * kGrStages * Shape::kSlot;
   const int rank = blockIdx.x % p.N, cid = blockIdx.x / p.N;
   const int b = cid / p.n_blk, c0 = cid % p.n_blk * kCols, c = c0 + pair;
-  const int len = gr_length(p.lengths, b, p.L), end = max(len, 0);
+  const int len = gr_length(sh, p.lengths, b, p.L), end = max(len, 0);
   const bool live = c < p.D && len >= 0, two = c + 1 < p.D;
   const int cols = min(p.D - c0, kCols);
   const T* x = static_cast<const T*>(p.x) + (size_t)b * p.L * p.D + c0;
@@ -299,7 +303,7 @@ __global__ void __launch_bounds__(kGrThreads, 2) gatedrec_fwd_kernel(const GrFwd
   F2 h = f2(0.0f, 0.0f);
   if (live && p.h0) h = gr_load<kPair>(p.h0 + (size_t)b * p.D + c, two);
 
-  const int rounds = (p.L + p.N * kTile - 1) / (p.N * kTile);
+  const int rounds = (end + p.N * kTile - 1) / (p.N * kTile);
   auto fetch = [&](int k) {
     if (k < rounds) {
       T* slot = ring + k % kGrStages * Shape::kSlot;
@@ -361,6 +365,14 @@ __global__ void __launch_bounds__(kGrThreads, 2) gatedrec_fwd_kernel(const GrFwd
       }
     }
   }
+  if (live) {
+    for (int i = rounds * p.N * kTile + (rank * kGrWarps + w) * G + grp; i < p.L;
+         i += p.N * kGrWarps * G)
+      gr_store<kPair>(y + (size_t)i * p.D + c, f2(0.0f, 0.0f), two);
+    if (p.h_chunks && rank == 0)
+      for (int i = rounds * p.N * kTile / kGrChunk + w * G + grp; i < n_chunks; i += kGrWarps * G)
+        gr_store<kPair>(p.h_chunks + ((size_t)b * n_chunks + i) * p.D + c, f2(0.0f, 0.0f), two);
+  }
   gr_cluster_end(p.N, ok);
   if (p.h_last) {
     if (live && rank == 0 && w == 0 && grp == 0) gr_store<kPair>(p.h_last + (size_t)b * p.D + c, h, two);
@@ -403,7 +415,7 @@ __global__ void __launch_bounds__(kGrThreads, 2) gatedrec_bwd_kernel(const GrBwd
   T* ring = reinterpret_cast<T*>(gr_smem + Shape::kShared) + w * kGrStages * Shape::kSlot;
   const int rank = blockIdx.x % p.N, cid = blockIdx.x / p.N;
   const int b = cid / p.n_blk, c0 = cid % p.n_blk * kCols, c = c0 + pair;
-  const int len = gr_length(p.lengths, b, p.L), end = max(len, 0);
+  const int len = gr_length(sh, p.lengths, b, p.L), end = max(len, 0);
   const bool live = c < p.D && len >= 0, two = c + 1 < p.D;
   const int cols = min(p.D - c0, kCols);
   const size_t seq = (size_t)b * p.L * p.D;
@@ -416,7 +428,7 @@ __global__ void __launch_bounds__(kGrThreads, 2) gatedrec_bwd_kernel(const GrBwd
   F2 l = zero;  // a_{t+1} l_{t+1} at the end of the round
   if (live && p.dh_last) l = gr_load<kPair>(p.dh_last + (size_t)b * p.D + c, two);
 
-  const int rounds = (p.L + p.N * kTile - 1) / (p.N * kTile);
+  const int rounds = (end + p.N * kTile - 1) / (p.N * kTile);
   auto first = [&](int k) { return ((rounds - 1 - k) * p.N + rank) * kTile; };  // the tile's token
   auto fetch = [&](int k) {
     if (k < rounds) {
@@ -495,6 +507,13 @@ __global__ void __launch_bounds__(kGrThreads, 2) gatedrec_bwd_kernel(const GrBwd
           gr_store<kPair>(dg + at, dxv * xv[s] * a[s], two);
         }
       }
+    }
+  }
+  if (live) {
+    for (int i = rounds * p.N * kTile + (rank * kGrWarps + w) * G + grp; i < p.L;
+         i += p.N * kGrWarps * G) {
+      gr_store<kPair>(p.dx + seq + (size_t)i * p.D + c, zero, two);
+      gr_store<kPair>(p.dg + seq + (size_t)i * p.D + c, zero, two);
     }
   }
   gr_cluster_end(p.N, ok);
