@@ -181,7 +181,9 @@ __device__ __forceinline__ bool gr_round(GrShared& sh, int k, int w, int r, int 
       if (i == r) enter = h;
       map_apply(h, map_load(&sh.cta[buf][i][l]));
     }
-    for (int i = 0; i < w; ++i) map_apply(enter, map_load(&sh.warp[buf][i][l]));
+#pragma unroll
+    for (int i = 0; i < kGrWarps - 1; ++i)
+      if (i < w) map_apply(enter, map_load(&sh.warp[buf][i][l]));
   } else {
 #pragma unroll
     for (int i = 0; i < kGrWarps; ++i) {
@@ -487,7 +489,9 @@ __global__ void __launch_bounds__(kGrThreads, 2) gatedrec_bwd_kernel(const GrBwd
     ok = gr_round<G, true>(sh, k, kGrWarps - 1 - w, p.N - 1 - rank, G - 1 - grp, p.N, lane, q, l,
                            e, ok, [&](int r) { return p.N - 1 - r; });
     if (live) {
-      for (int i = 0; i < w; ++i) map_apply(h, map_load(&fwd[k & 1][i][pair / 2]));
+#pragma unroll
+      for (int i = 0; i < kGrWarps - 1; ++i)
+        if (i < w) map_apply(h, map_load(&fwd[k & 1][i][pair / 2]));
       map_apply(h, groups);
 #pragma unroll
       for (int s = 0; s < S; ++s) {
