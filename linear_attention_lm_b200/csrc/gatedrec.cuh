@@ -95,18 +95,18 @@ __device__ __forceinline__ F2 f2_shfl(F2 a, int src) {
 template <int G, bool kBack>
 __device__ __forceinline__ GrMap map_scan_groups(GrMap& m, int o, int lane) {
   constexpr int W = 32 / G;
-  if constexpr (G > 1) {
+  GrMap before = map_one();
 #pragma unroll
-    for (int d = 1; d < G; d *= 2) {
-      const int src = (kBack ? lane + d * W : lane - d * W) & 31;
-      const GrMap prev{f2_shfl(m.A, src), f2_shfl(m.H, src)};
-      if (o >= d) map_after(m, prev);
-    }
-    const int src = (kBack ? lane + W : lane - W) & 31;
+  for (int d = 1; d < G; d *= 2) {
+    const int src = (kBack ? lane + d * W : lane - d * W) & 31;
     const GrMap prev{f2_shfl(m.A, src), f2_shfl(m.H, src)};
-    if (o > 0) return prev;
+    if (o >= d) {
+      if (d == 1) before = prev;
+      else map_after(before, prev);
+      map_after(m, prev);
+    }
   }
-  return map_one();
+  return before;
 }
 __device__ __forceinline__ void map_apply(F2& h, const GrMap& m) { h = f2_fma(m.A, h, m.H); }
 
@@ -501,15 +501,21 @@ __global__ void __launch_bounds__(kGrThreads, 2) gatedrec_bwd_kernel(const GrBwd
       }
         float *dx = p.dx + seq + (size_t)first(k) * p.D, *dg = p.dg + seq + (size_t)first(k) * p.D;
       uint32_t at = (uint32_t)((w * G + grp) * S + S - 1) * p.D + c;
-#pragma unroll
-      for (int s = S - 1; s >= 0; --s, at -= p.D) {
+      auto step = [&](int s, bool in) {
         const F2 lt = e + d[s];
         const F2 dxv = n[s] * lt;  // past the end n is 0
         e = a[s] * lt;
-        if (t0 + s < p.L) {
+        if (in) {
           gr_store<kPair>(dx + at, dxv, two);
           gr_store<kPair>(dg + at, dxv * xv[s] * a[s], two);
         }
+      };
+      if (t0 + S <= p.L) {
+#pragma unroll
+        for (int s = S - 1; s >= 0; --s, at -= p.D) step(s, true);
+      } else {
+#pragma unroll
+        for (int s = S - 1; s >= 0; --s, at -= p.D) step(s, t0 + s < p.L);
       }
     }
   }
