@@ -21,10 +21,17 @@ namespace based {
 constexpr int kLnThreads = 256;   // threads of a CTA (more only for the longest rows)
 constexpr int kLnMaxD = 16384;
 
+// Barrier of the threads of a row.  Rows of several warps have a named barrier of
+// their own, so the rows of a CTA run at their own pace.
+__device__ __forceinline__ void row_barrier(int warp, int row_warps) {
+  if (row_warps == 1) __syncwarp();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / row_warps), "r"(row_warps * 32) : "memory");
+}
+
 // Sums of N values over the threads of a row: row_warps warps of the CTA, this
 // one the wr-th.  `red` holds N floats per warp and is free again after the
-// row's next barrier.  Rows of several warps have a named barrier of their own,
-// so the rows of a CTA run at their own pace.
+// row's next barrier.
 template <int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], float* red, int warp, int wr,
                                         int row_warps) {
@@ -35,7 +42,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* red, int warp, int
 #pragma unroll
     for (int n = 0; n < N; ++n) red[warp * N + n] = v[n];
   }
-  asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / row_warps), "r"(row_warps * 32) : "memory");
+  row_barrier(warp, row_warps);
   const float* r = red + (warp - wr) * N;
 #pragma unroll
   for (int n = 0; n < N; ++n) {
@@ -151,22 +158,50 @@ struct LnBwdParams {
 // dbias in registers; the groups of the CTA meet in shared memory at the end, and
 // the CTA writes one part [2][D] (fp32).  Vectors are four values at most: 16
 // bytes of the fp32 arrays, which are most of the traffic.  The rows to come are
-// copied ahead by cp.async into slots that only the copying thread reads, so no
-// barrier is between a row's arrival and its use.
+// copied ahead by cp.async.  Where rows are whole vectors of four, each thread
+// copies what it will read itself and no barrier is between a row's arrival and its
+// use; other rows are copied as the 16-byte pieces that hold them, by the whole
+// group (3001 x 999 fp32: 19.8 us with 4-byte copies, 18.2 with pieces; 16384 x 999 bf16, where
+// two-byte copies have no asynchronous form: 148 and 72 us).
 template <typename T, int V, int E, int kThreads>
 struct LnBwdShape {
   static constexpr int NV = E / V;
-  // two-byte copies have no asynchronous form, and the longest rows no room
-  static constexpr bool kAsync = V * sizeof(T) >= 4 && kThreads <= 512;
+  static constexpr bool kAhead = kThreads <= 512;  // the longest rows leave no room
+  static constexpr bool kOwn = kAhead && V == 4, kShare = kAhead && V < 4;
   static constexpr int kStages = sizeof(T) == 2 ? 3 : 2;  // two CTAs of 256 threads fit an SM
   static constexpr int kX = V * (int)sizeof(T), kR = V * 4;  // bytes of a vector
   static constexpr int kThread = NV * (2 * kX + kR);         // bytes of a thread's row
+  // a row of n bytes starts anywhere in its first 16-byte piece
+  __host__ __device__ static constexpr int pieces(int n) { return (n + 15 + 15) / 16 * 16; }
+  __host__ __device__ static constexpr int shared_row(int D) {
+    return 2 * pieces(D * (int)sizeof(T)) + pieces(D * 4);
+  }
   static size_t smem(int tpr, int D) {
-    const size_t ring = kAsync ? (size_t)kStages * kThread * kThreads : 0;
-    const size_t join = tpr < kThreads ? (size_t)D * 8 : 0;
+    const size_t ring = kOwn     ? (size_t)kStages * kThread * kThreads
+                        : kShare ? (size_t)kStages * shared_row(D) * (kThreads / tpr)
+                                 : 0;
+    const size_t join = tpr < kThreads ? (size_t)D * 8 * (kThreads / tpr) : 0;
     return join > ring ? join : ring;
   }
 };
+
+// The row of D values at element `row * D` of an array of n values, as 16-byte
+// pieces, into `to`, by the tpr threads of a group.
+template <typename T>
+__device__ __forceinline__ void copy_row_pieces(unsigned char* to, const T* from, long long row,
+                                                int D, long long n, int lane, int tpr) {
+  const long long begin = row * D * (long long)sizeof(T), first = begin & ~15LL;
+  const int len = (int)(begin - first) + D * (int)sizeof(T);
+  const long long all = n * (long long)sizeof(T);
+  const unsigned char* src = reinterpret_cast<const unsigned char*>(from) + first;
+  for (int o = lane * 16; o < len; o += tpr * 16)
+    umma::cp_async16_part(to + o, src + o, (int)min(16LL, all - first - o));
+}
+// Where the row's first value lies in its pieces.
+template <typename T>
+__device__ __forceinline__ int row_shift(long long row, int D) {
+  return (int)(row * D * (long long)sizeof(T) & 15);
+}
 
 template <int Bytes>
 __device__ __forceinline__ void copy_async(void* to, const void* from) {
@@ -194,24 +229,41 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 && E <= 16 ? 2 : 1)
     for (int e = 0; e < V; ++e) w[i][e] = dw[i][e] = db[i][e] = 0.0f;
     if (c < p.D) load_f32<V>(p.w + c, w[i]);
   }
-  // slot of (stage, array, vector i): [thread] vectors
-  auto slot = [&](int stage, int array, int i) {
-    unsigned char* s = ln_smem + (size_t)stage * Shape::kThread * blockDim.x;
-    return s + (array * NV * Shape::kX + i * (array == 2 ? Shape::kR : Shape::kX)) * blockDim.x +
-           threadIdx.x * (array == 2 ? Shape::kR : Shape::kX);
+  // vector i of array (0: x, 1: dy, 2: dresid) of this thread's row in a stage
+  auto slot = [&](int stage, int array, int i, long long row) -> unsigned char* {
+    const int size = array == 2 ? Shape::kR : Shape::kX;
+    if constexpr (Shape::kOwn) {
+      return ln_smem + ((size_t)stage * Shape::kThread + array * NV * Shape::kX + i * size) * kThreads +
+             threadIdx.x * size;
+    } else {
+      return ln_smem + (size_t)(stage * rpb + warp / p.row_warps) * Shape::shared_row(p.D) +
+             array * Shape::pieces(p.D * (int)sizeof(T)) +
+             (array == 2 ? row_shift<float>(row, p.D) : row_shift<T>(row, p.D)) +
+             (i * tpr + lane) * size;
+    }
   };
   const T *x = static_cast<const T*>(p.x), *dy = static_cast<const T*>(p.dy);
   auto fetch = [&](long long row, int stage) {
     if (row < p.rows) {
-      const size_t off = (size_t)row * p.D;
+      if constexpr (Shape::kOwn) {
+        const size_t off = (size_t)row * p.D;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * tpr + lane) * V;
-        if (c < p.D) {
-          copy_async<Shape::kX>(slot(stage, 0, i), x + off + c);
-          copy_async<Shape::kX>(slot(stage, 1, i), dy + off + c);
-          if (p.dresid) copy_async<Shape::kR>(slot(stage, 2, i), p.dresid + off + c);
+        for (int i = 0; i < NV; ++i) {
+          const int c = (i * tpr + lane) * V;
+          if (c < p.D) {
+            copy_async<Shape::kX>(slot(stage, 0, i, row), x + off + c);
+            copy_async<Shape::kX>(slot(stage, 1, i, row), dy + off + c);
+            if (p.dresid) copy_async<Shape::kR>(slot(stage, 2, i, row), p.dresid + off + c);
+          }
         }
+      } else {
+        unsigned char* s =
+            ln_smem + (size_t)(stage * rpb + warp / p.row_warps) * Shape::shared_row(p.D);
+        const int size = Shape::pieces(p.D * (int)sizeof(T));
+        const long long n = p.rows * p.D;
+        copy_row_pieces(s, x, row, p.D, n, lane, tpr);
+        copy_row_pieces(s + size, dy, row, p.D, n, lane, tpr);
+        if (p.dresid) copy_row_pieces(s + 2 * size, p.dresid, row, p.D, n, lane, tpr);
       }
     }
     umma::cp_async_commit();
@@ -219,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 && E <= 16 ? 2 : 1)
   const float inv_d = 1.0f / p.D;
   const long long step = (long long)gridDim.x * rpb;
   long long row = (long long)blockIdx.x * rpb + warp / p.row_warps;
-  if constexpr (Shape::kAsync) {
+  if constexpr (Shape::kAhead) {
 #pragma unroll
     for (int k = 0; k < kStages - 1; ++k) fetch(row + k * step, k);
   }
@@ -231,16 +283,17 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 && E <= 16 ? 2 : 1)
     float next_mean = 0.0f, next_rstd = 0.0f;
     if (row + step < p.rows) next_mean = p.mean[row + step], next_rstd = p.rstd[row + step];
     Pack<T, V> xv[NV], gv[NV];
-    if constexpr (Shape::kAsync) umma::cp_async_wait<kStages - 2>();
+    if constexpr (Shape::kAhead) umma::cp_async_wait<kStages - 2>();
+    if constexpr (Shape::kShare) row_barrier(warp, p.row_warps);  // and the row before is done with
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * tpr + lane) * V;
       xv[i].zero();
       gv[i].zero();
       if (c < p.D) {
-        if constexpr (Shape::kAsync) {
-          xv[i].load(reinterpret_cast<const T*>(slot(stage, 0, i)));
-          gv[i].load(reinterpret_cast<const T*>(slot(stage, 1, i)));
+        if constexpr (Shape::kAhead) {
+          xv[i].load(reinterpret_cast<const T*>(slot(stage, 0, i, row)));
+          gv[i].load(reinterpret_cast<const T*>(slot(stage, 1, i, row)));
         } else {
           xv[i].load(x + off + c);
           gv[i].load(dy + off + c);
@@ -248,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 && E <= 16 ? 2 : 1)
       }
     }
     // into the slot of the row before
-    if constexpr (Shape::kAsync)
+    if constexpr (Shape::kAhead)
       fetch(row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
     float s[2] = {0.0f, 0.0f};
     float xh[NV][V];
@@ -274,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 && E <= 16 ? 2 : 1)
 #pragma unroll
         for (int e = 0; e < V; ++e) d[e] = 0.0f;
         if (p.dresid)
-          load_f32<V>(Shape::kAsync ? reinterpret_cast<const float*>(slot(stage, 2, i))
+          load_f32<V>(Shape::kAhead ? reinterpret_cast<const float*>(slot(stage, 2, i, row))
                                     : p.dresid + off + c,
                       d);
 #pragma unroll
@@ -287,39 +340,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 && E <= 16 ? 2 : 1)
     rstd = next_rstd;
     stage = stage + 1 == kStages ? 0 : stage + 1;
   }
-  if constexpr (Shape::kAsync) umma::cp_async_wait<0>();
-  // rows of the CTA together: group 0 adds the others' sums in order
+  if constexpr (Shape::kAhead) umma::cp_async_wait<0>();
+  // the groups of the CTA together, in order
   float* part = p.parts + (size_t)blockIdx.x * 2 * p.D;
-  float* join = reinterpret_cast<float*>(ln_smem);
-  for (int grp = rpb - 1; grp > 0; --grp) {
-    __syncthreads();
-    if (warp / p.row_warps == grp) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * tpr + lane) * V;
-        if (c < p.D)
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            join[c + e] = dw[i][e];
-            join[p.D + c + e] = db[i][e];
-          }
-      }
-    }
-    __syncthreads();
-    if (warp / p.row_warps == 0) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * tpr + lane) * V;
-        if (c < p.D)
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            dw[i][e] += join[c + e];
-            db[i][e] += join[p.D + c + e];
-          }
-      }
-    }
-  }
-  if (warp / p.row_warps == 0) {
+  if (rpb == 1) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * tpr + lane) * V;
@@ -328,6 +352,30 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 && E <= 16 ? 2 : 1)
         store_f32<V>(part + p.D + c, db[i]);
       }
     }
+    return;
+  }
+  float* join = reinterpret_cast<float*>(ln_smem);  // [group][2][D]
+  float* own = join + (size_t)(warp / p.row_warps) * 2 * p.D;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * tpr + lane) * V;
+    if (c < p.D) {
+      store_f32<V>(own + c, dw[i]);
+      store_f32<V>(own + p.D + c, db[i]);
+    }
+  }
+  __syncthreads();
+#pragma unroll 4
+  for (int c = threadIdx.x * V; c < 2 * p.D; c += kThreads * V) {
+    float s[V], o[V];
+    load_f32<V>(join + c, s);
+    for (int g = 1; g < rpb; ++g) {
+      load_f32<V>(join + (size_t)g * 2 * p.D + c, o);
+#pragma unroll
+      for (int e = 0; e < V; ++e) s[e] += o[e];
+    }
+    store_f32<V>(part + c, s);
   }
 }
 

@@ -127,6 +127,12 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool vali
                "r"(valid ? 16 : 0)
                : "memory");
 }
+// The same reading only the first `bytes` (0 to 16); the rest becomes zero.
+__device__ __forceinline__ void cp_async16_part(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(bytes)
+               : "memory");
+}
 // The same for 4 or 8 bytes (aligned to their size).
 template <int Bytes>
 __device__ __forceinline__ void cp_async_small(void* dst, const void* src, bool valid) {
