@@ -451,8 +451,10 @@ based_status_t based_gatedrec_step(const void* x, const void* g, float* h, void*
  *              the V tile load of its second chunk;
  *   which = 2  the first CTA of the window attention (bf16) leaves out its V
  *              tile load;
+ *   which = 3  the first CTA of the gated recurrence, where it runs in clusters,
+ *              leaves out one of its sends to another CTA in the first round;
  * and the time after which every bounded wait gives up, wait_limit_ns > 0
- * (2e9, two seconds, is the default).  A wait on a load that was left out runs
+ * (2e9, two seconds, is the default).  A wait on a load or send that was left out runs
  * out: the kernel records BASED_ERR_TIMEOUT (see based_get_device_error),
  * drains its own loads and stores in flight, releases its tensor memory and
  * returns; its outputs are then undefined.  Nothing faults and nothing is

@@ -725,11 +725,11 @@ def based_gatedrec_step(x, g, h, y, stream=None):
     return y
 
 
-STALL_NONE, STALL_LINATTN_V, STALL_WINDOW_V = 0, 1, 2
+STALL_NONE, STALL_LINATTN_V, STALL_WINDOW_V, STALL_GATEDREC = 0, 1, 2, 3
 
 
 def based_debug_stall(which: int, wait_limit_ns: int = 2_000_000_000):
-    """Test hook: make the first CTA of the chosen kernel leave one load out
+    """Test hook: make the first CTA of the chosen kernel leave one load (or send) out
     so its bounded wait runs out after wait_limit_ns (which = 0 restores
     normal operation)."""
     _check("based_debug_stall", load_library().based_debug_stall(int(which), int(wait_limit_ns)))

@@ -876,7 +876,8 @@ based_status_t based_baseconv_fwd(const void* x, const void* w, const float* bia
 }
 
 based_status_t based_debug_stall(int which, long long wait_limit_ns) {
-  if (which != kStallNone && which != kStallLinattnV && which != kStallWindowV)
+  if (which != kStallNone && which != kStallLinattnV && which != kStallWindowV &&
+      which != kStallGatedrec)
     return BASED_ERR_INVALID_ARG;
   if (wait_limit_ns <= 0) return BASED_ERR_INVALID_ARG;
   const uint64_t limit = static_cast<uint64_t>(wait_limit_ns);

@@ -29,6 +29,7 @@ __device__ __forceinline__ void record_device_error(int code) {
 constexpr int kStallNone = 0;
 constexpr int kStallLinattnV = 1;  // linear-attention prefill: the V tile of its second chunk
 constexpr int kStallWindowV = 2;   // window attention: its V tile
+constexpr int kStallGatedrec = 3;  // gated recurrence: a map sent to another CTA of its cluster
 __device__ int g_stall_test = kStallNone;
 
 __device__ __forceinline__ bool stall_test(int which) {

@@ -150,6 +150,11 @@ __device__ __forceinline__ void gr_cluster_end(int N, bool ok) {
   __syncwarp();
   if (N > 1) umma::cluster_sync();
   else __syncthreads();
+  if (!ok) {  // sends that this CTA did not wait for have long been issued: let them land
+    const uint64_t t0 = umma::global_timer_ns();
+    while (umma::global_timer_ns() - t0 < 100000) {
+    }
+  }
 }
 
 // One round k: every lane of the cluster gives its map `mine`.  w, r and o are the
@@ -170,13 +175,15 @@ __device__ __forceinline__ bool gr_round(GrShared& sh, int k, int w, int r, int 
       GrMap all = map_load(&sh.warp[buf][0][l]);
 #pragma unroll
       for (int i = 1; i < kGrWarps; ++i) map_then(all, map_load(&sh.warp[buf][i][l]));
-      if (o == 0)
+      if (o == 0 && !(k == 0 && w == 1 && stall_test(kStallGatedrec)))
         umma::st_async_16(umma::cluster_addr(&sh.cta[buf][r][l], (uint32_t)to(w)), all.A.v, all.H.v,
                           umma::cluster_addr(&sh.bar[buf], (uint32_t)to(w)));
     }
     if (ok) ok = umma::mbar_wait_cluster_inline(&sh.bar[buf], (k >> 1) & 1);
-    if (threadIdx.x == 0 && ok)
-      umma::mbar_arrive_expect_tx(&sh.bar[buf], gr_round_bytes<G>(N));  // for round k + 2
+    if (threadIdx.x == 0) {  // for round k + 2
+      if (ok) umma::mbar_arrive_expect_tx(&sh.bar[buf], gr_round_bytes<G>(N));
+      else umma::mbar_expect_tx(&sh.bar[buf], gr_round_bytes<G>(N));  // no wait: bytes that still come
+    }
     for (int i = 0; i < N; ++i) {
       if (i == r) enter = h;
       map_apply(h, map_load(&sh.cta[buf][i][l]));

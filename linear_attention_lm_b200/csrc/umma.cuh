@@ -533,6 +533,12 @@ __device__ __forceinline__ void st_async_16(uint32_t dst, uint64_t a, uint64_t b
       "l"(a), "l"(b), "r"(bar)
       : "memory");
 }
+// Add to the transaction bytes of the current phase, without arriving.
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+               "r"(bytes)
+               : "memory");
+}
 // Bounded wait for a phase that CTAs of the cluster complete (as mbar_wait_cluster,
 // without a call, for kernels that hold many registers across it).
 __device__ __forceinline__ bool mbar_wait_cluster_inline(uint64_t* bar, uint32_t parity) {

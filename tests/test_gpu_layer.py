@@ -330,7 +330,8 @@ def rec_bounds(x, g, h0, dy=None, dh=None, lengths=None):
 
 
 REC_SIZES = [(1, 1, 1), (3, 2, 33), (2, 63, 64), (1, 64, 100), (2, 65, 1000), (4, 130, 256),
-             (1, 700, 40), (1, 1025, 1024), (2, 257, 2050), (5, 31, 8), (1, 4100, 72), (40, 20, 64)]
+             (1, 700, 40), (1, 1025, 1024), (2, 257, 2050), (5, 31, 8), (1, 4100, 72), (40, 20, 64),
+             (3, 3000, 24)]
 
 
 def rec_inputs(B, L, D, dtype, ragged):
@@ -500,6 +501,26 @@ def test_gatedrec_state_in_place_and_bits():
     lab.based_gatedrec_bwd(x, g, x, first[2], torch.empty_like(grads[0]), torch.empty_like(grads[1]),
                            h, h)
     assert torch.equal(h, grads[2])
+
+
+def test_gatedrec_wait_runs_out_then_recovers():
+    """One CTA of a cluster leaves out a send: the receiver gives up after 1 ms, the
+    error is recorded, nothing faults, and the next call is as the first."""
+    x, g = gen(1, (1, 6000, 64), "bf16"), gen(2, (1, 6000, 64), "bf16")
+    first = lab.gatedrec(x, g, return_state=True, for_grad=True)
+    grads = lab.gatedrec_grad(x, g, x, first[2])
+    assert lab.based_get_device_error() == 0
+    for call in (lambda: lab.gatedrec(x, g), lambda: lab.gatedrec_grad(x, g, x, first[2])):
+        lab.based_debug_stall(lab.STALL_GATEDREC, 1_000_000)
+        try:
+            call()
+            assert lab.based_get_device_error() == 4
+        finally:
+            lab.based_debug_stall(lab.STALL_NONE, 2_000_000_000)
+    again = lab.gatedrec(x, g, return_state=True, for_grad=True)
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
+    assert all(torch.equal(a, b) for a, b in zip(grads, lab.gatedrec_grad(x, g, x, first[2])))
+    assert lab.based_get_device_error() == 0
 
 
 # ------------------------------------------------------------------ together
