@@ -9,6 +9,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <numeric>
 #include <type_traits>
 
 #include "based.h"

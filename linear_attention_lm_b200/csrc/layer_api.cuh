@@ -118,19 +118,19 @@ based_status_t check_layernorm(long long rows, int D, based_dtype_t dt) {
 
 based_status_t launch_rotary(RotaryParams p, int B, bool interleaved, based_dtype_t dt,
                              cudaStream_t st) {
-  // 2V values per chunk: V has to divide half of the turned part and the head
-  const long long n = (p.rot / 2) % 8 == 0 && p.D % 8 == 0   ? 8
-                      : (p.rot / 2) % 4 == 0 && p.D % 4 == 0 ? 4
-                      : (p.rot / 2) % 2 == 0 && p.D % 2 == 0 ? 2
-                                                             : 1;
+  // 2V values per chunk in two vectors: V has to divide the head and, where the
+  // pairs are halves apart, half of the turned part
+  const long long n = interleaved ? p.D : std::gcd(p.D, p.rot / 2);
   return for_vector(dt, n, [&](auto t, auto v) -> based_status_t {
     using T = decltype(t);
     constexpr int V = decltype(v)::value;
     RotaryParams r = p;
-    r.rot_chunks = r.rot / (2 * V);
+    r.rot_chunks = (int)ceil_div(r.rot, 2 * V);
     r.chunks = r.rot_chunks;
     const bool in_place = (!r.H_q || r.q == r.q_out) && (!r.H_k || r.k == r.k_out);
-    if (!in_place) r.chunks += (int)ceil_div(r.D - r.rot, 2 * V);
+    if (!in_place)
+      r.chunks = (int)(interleaved ? ceil_div(r.D, 2 * V)
+                                   : r.rot_chunks + ceil_div(r.D - r.rot, 2 * V));
     r.items = (long long)B * r.L * r.chunks;
     const long long blocks = ceil_div(r.items, kRotThreads);
     if (blocks > 0x7fffffffLL) return BASED_ERR_UNSUPPORTED;

@@ -30,8 +30,8 @@ struct RotaryParams {
   long long pos0;
   long long items;  // B * L * chunks
   int L, D, rot, H_q, H_k;
-  int chunks;     // of 2V values of a head: turned ones, then those that pass
-  int rot_chunks;
+  int chunks;      // of 2V values of a head: turned ones, then those that pass
+  int rot_chunks;  // (interleaved: the last may hold values that pass)
   int heads_per_cta;
   float mscale;   // negative sine: inverse
   float sign;
@@ -57,19 +57,21 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
   pos += t;
   const bool turned = ch < p.rot_chunks;
   // the chunk's two vectors of V values
-  int c0, c1;
-  if (turned) {
-    c0 = kInter ? 2 * ch * V : ch * V;
-    c1 = kInter ? c0 + V : c0 + p.rot / 2;
-  } else {
-    c0 = p.rot + 2 * (ch - p.rot_chunks) * V;
-    c1 = c0 + V;
+  int c0 = 2 * ch * V, c1 = c0 + V;
+  if (!kInter) {
+    c0 = turned ? ch * V : p.rot + 2 * (ch - p.rot_chunks) * V;
+    c1 = c0 + (turned ? p.rot / 2 : V);
   }
   const bool two = c1 < p.D;
   float cs[V], sn[V];
   if (turned) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
+      if (kInter && ch * V + i >= p.rot / 2) {
+        cs[i] = 1.0f;
+        sn[i] = 0.0f;
+        continue;
+      }
       const double turns = (double)pos * p.freqs[ch * V + i];
       const float part = (float)(turns - rint(turns));
       float s, c;
