@@ -218,17 +218,18 @@ __device__ __forceinline__ void gr_fetch(T* slot, const T* src, int D, int t0, i
     else if constexpr (CW >= 4) umma::cp_async_small<CW>(to, from, in);
     else *to = in ? *from : from_f32<T>(0.0f);
   };
-  if constexpr (CW == 16) {  // nothing outside: a start and constant steps
+  if constexpr (CW == 16) {  // every token inside: a start and constant steps
     constexpr int R = 32 / RC;  // rows per copy instruction
     static_assert(RC <= 32 && (S % R == 0 || R % S == 0), "the step of a row is a constant");
-    if (t0 + G * S <= end && cols == kCols) {
+    if (t0 + G * S <= end) {
       const int row = lane / RC, col = lane % RC * E;
-      const T* from = src + ((size_t)(t0 + row) * D + col);
+      const bool in = col < cols;
+      const T* from = src + (in ? (size_t)(t0 + row) * D + col : 0);
       T* to = slot + (row % S * G + row / S) * kCols + col;
-      const size_t step = (size_t)R * D;
+      const size_t step = in ? (size_t)R * D : 0;
 #pragma unroll
       for (int i = 0; i < S * G / R; ++i, from += step)
-        copy(to + (i * R % S * G + i * R / S) * kCols, from, true);
+        copy(to + (i * R % S * G + i * R / S) * kCols, from, in);
       return;
     }
   }

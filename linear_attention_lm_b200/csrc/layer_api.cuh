@@ -233,12 +233,15 @@ bool launch_gatedrec(void (*kern)(P), const P& p, long long clusters, size_t sme
 // (8 x 2048 x 1024 bf16: forward 24.2 us with G = 2, N = 1, 27.6 with G = 1, N = 2 and
 // 28.1 with neither; gradient 46.7, 58.1 and 54.4), but rows of 32 bytes (G = 4) lose
 // to eight CTAs (1 x 16384 x 1024: forward 31.4 us with G = 2, N = 8, 33.5 with G = 4,
-// N = 4), so G = 4 is for fewer channels than eight CTAs fill the GPU with.
+// N = 4), so G = 4 is for fewer channels than eight CTAs fill the GPU with.  A padded
+// batch leaves SMs to its longest sequences early: twice the CTAs, and G = 4 before
+// clusters (8 sequences of 0 to 2048 tokens x 1024: forward 19.6 us, gradient 35.7;
+// as for full sequences 22.4 and 44.3; G = 2, N = 2: 21.6 and 40.6).
 struct GrPlan {
   int G, N, n_blk;
 };
-inline GrPlan plan_gatedrec(int B, int L, int D, int group_tokens) {
-  const long long slots = 2LL * device_sm_count();
+inline GrPlan plan_gatedrec(int B, int L, int D, int group_tokens, bool padded) {
+  const long long slots = (padded && B > 1 ? 4LL : 2LL) * device_sm_count();
   auto cut = [&](int G) {
     GrPlan pl{G, 1, (int)ceil_div(D, 64 / G)};
     const long long clusters = (long long)B * pl.n_blk, tile = (long long)G * kGrWarps * group_tokens;
@@ -251,7 +254,7 @@ inline GrPlan plan_gatedrec(int B, int L, int D, int group_tokens) {
   };
   GrPlan pl = cut(1);
   if (more(2)) pl = cut(2);
-  if (pl.G == 2 && more(4) && (long long)B * pl.n_blk * pl.N * 2 <= slots) pl = cut(4);
+  if (pl.G == 2 && more(4) && (padded || (long long)B * pl.n_blk * pl.N * 2 <= slots)) pl = cut(4);
   return pl;
 }
 
@@ -380,7 +383,7 @@ based_status_t based_gatedrec_fwd(const void* x, const void* g, void* y, const f
   return for_copies(dt, D, [&](auto t, auto cw) -> based_status_t {
     using T = decltype(t);
     constexpr int CW = decltype(cw)::value;
-    const GrPlan pl = plan_gatedrec(B, L, D, GrFwdShape<T, 1>::S);
+    const GrPlan pl = plan_gatedrec(B, L, D, GrFwdShape<T, 1>::S, lengths != nullptr);
     p.n_blk = pl.n_blk;
     p.N = pl.N;
     const long long clusters = (long long)B * pl.n_blk;
@@ -412,7 +415,7 @@ based_status_t based_gatedrec_bwd(const void* x, const void* g, const void* dy,
   return for_copies(dt, D, [&](auto t, auto cw) -> based_status_t {
     using T = decltype(t);
     constexpr int CW = decltype(cw)::value;
-    const GrPlan pl = plan_gatedrec(B, L, D, GrBwdShape<T, 1>::S);
+    const GrPlan pl = plan_gatedrec(B, L, D, GrBwdShape<T, 1>::S, lengths != nullptr);
     p.n_blk = pl.n_blk;
     p.N = pl.N;
     const long long clusters = (long long)B * pl.n_blk;
