@@ -660,3 +660,67 @@ def test_a_layer_and_its_gradient():
     for got, ref in zip((dr, dw, db), want):
         assert np.linalg.norm(f64(got) - ref) <= 2.0 ** -15 * np.linalg.norm(ref)
     assert lab.based_get_device_error() == 0
+
+
+def test_offsets_past_32_bits():
+    """Tensors of over 2^31 elements: what lies at their ends is what a call on the
+    ends alone gives, bit for bit."""
+    def fill(shape, seed, dtype=torch.bfloat16):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        t = torch.empty(shape, dtype=dtype, device="cuda")
+        flat = t.view(-1)
+        flat[:1 << 20].normal_(generator=g)
+        flat[-(1 << 28):].normal_(generator=g)
+        flat[1 << 20:-(1 << 28)] = 0.5
+        return t
+
+    rows, D = (1 << 21) + 5, 1024
+    x, w = fill((rows, D), 1), gen(2, (D,))
+    y, mean, rstd = lab.layernorm(x, w, return_stats=True)
+    for part in (slice(0, 64), slice(rows - 64, rows)):
+        want = lab.layernorm(x[part].contiguous(), w, return_stats=True)
+        assert all(torch.equal(a, b) for a, b in zip((y[part], mean[part], rstd[part]), want))
+    del y
+    dx, _, _ = lab.layernorm_grad(x, x, w, mean, rstd)
+    tail = slice(rows - 64, rows)
+    want = lab.layernorm_grad(x[tail].contiguous(), x[tail].contiguous(), w,
+                              mean[tail].clone(), rstd[tail].clone())[0]
+    assert torch.equal(dx[tail], want)
+    del x, dx
+    freqs, L = lab.rotary_freqs(128), (1 << 20) + 8
+    q = fill((1, 17, L, 128), 3)
+    out = lab.rotary(q, None, freqs, 7)[0]
+    assert torch.equal(out[:, -1:], lab.rotary(q[:, -1:].contiguous(), None, freqs, 7)[0])
+    del q, out
+    L, D, last = (1 << 20) + (1 << 14), 2048, 1 << 16
+    x, g = fill((1, L, D), 4), fill((1, L, D), 5)
+    y, h, chunks = lab.gatedrec(x, g, return_state=True, for_grad=True)
+    cut = L - last
+    tail = [t[:, cut:].contiguous() for t in (x, g)]
+    yt, ht, ct = lab.gatedrec(*tail, chunks[:, cut // 64].contiguous(), return_state=True,
+                              for_grad=True)
+    assert torch.equal(y[:, cut:], yt) and torch.equal(h, ht)
+    assert torch.equal(chunks[:, cut // 64:], ct)
+    del yt, y
+    dx, dg, _ = lab.gatedrec_grad(x, g, x, chunks)
+    del g
+    want = lab.gatedrec_grad(*tail, tail[0], ct)
+    assert torch.equal(dx[:, cut:], want[0]) and torch.equal(dg[:, cut:], want[1])
+    assert lab.based_get_device_error() == 0
+
+
+def test_raw_stream_handles_and_workspaces():
+    """A stream given by its handle, and a workspace of the caller's, give the same bits."""
+    x, w = gen(1, (300, 1000), "bf16"), gen(2, (1000,))
+    _, mean, rstd = lab.layernorm(x, w, return_stats=True)
+    want = lab.layernorm_grad(x, x, w, mean, rstd)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    nbytes = lab.based_layernorm_bwd_workspace_bytes(300, 1000)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    outs = [torch.empty_like(t) for t in want]
+    lab.based_layernorm_bwd(x, x, w, mean, rstd, *outs, workspace=ws, stream=side.cuda_stream)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    with pytest.raises(lab.BasedError):
+        lab.based_layernorm_bwd(x, x, w, mean, rstd, *outs, workspace=ws[:nbytes - 16])
