@@ -86,21 +86,33 @@ based_status_t launch_layernorm_bwd(LnBwdParams p, const LnBwdPlan& pl, float* d
                                     cudaStream_t st) {
   p.row_warps = pl.row_warps;
   if (pl.parts > 0) {
-    auto go = [&](auto n) {
+    auto go = [&](auto n, auto row_warps) {
       constexpr int kN = decltype(n)::value;
-      auto kern = layernorm_bwd_kernel<T, V, E, kN>;
+      auto kern = layernorm_bwd_kernel<T, V, E, kN, decltype(row_warps)::value>;
       const size_t smem = LnBwdShape<T, V, E, kN>::smem(pl.row_warps * 32, p.D);
       return set_smem(kern, smem) &&
              launch_dependent(kern, dim3((unsigned)pl.parts), dim3(kN), smem, st, p);
     };
-    using std::integral_constant;
+    constexpr std::integral_constant<int, 256> k256{};
+    constexpr std::integral_constant<int, 512> k512{};
+    constexpr std::integral_constant<int, 1024> k1024{};
+    constexpr std::integral_constant<int, 0> any{};
     bool ok;
-    if constexpr (E > 8) {
-      ok = pl.threads == 256   ? go(integral_constant<int, 256>{})
-           : pl.threads == 512 ? go(integral_constant<int, 512>{})
-                               : go(integral_constant<int, 1024>{});
+    if constexpr (E == 8) {
+      ok = go(k256, std::integral_constant<int, 1>{});
+    } else if constexpr (V == 4) {
+      switch (pl.row_warps) {
+        case 1: ok = go(k256, std::integral_constant<int, 1>{}); break;
+        case 2: ok = go(k256, std::integral_constant<int, 2>{}); break;
+        case 4: ok = go(k256, std::integral_constant<int, 4>{}); break;
+        case 8: ok = go(k256, std::integral_constant<int, 8>{}); break;
+        case 16: ok = go(k512, std::integral_constant<int, 16>{}); break;
+        default: ok = go(k1024, std::integral_constant<int, 32>{});
+      }
     } else {
-      ok = go(integral_constant<int, 256>{});
+      ok = pl.threads == 256   ? go(k256, any)
+           : pl.threads == 512 ? go(k512, any)
+                               : go(k1024, any);
     }
     if (!ok) return BASED_ERR_CUDA;
   }

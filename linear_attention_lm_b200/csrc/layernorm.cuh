@@ -209,34 +209,72 @@ __device__ __forceinline__ void copy_async(void* to, const void* from) {
   else umma::cp_async_small<Bytes>(to, from, true);
 }
 
-template <typename T, int V, int E, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads == 256 && E <= 16 ? 2 : 1)
+// A thread's NV vectors of V elements as pairs.  at(i): where vector i lies (aligned
+// to all its elements); in(i): whether it does (zeros if not).
+template <typename T, int V, int NV, typename At, typename In>
+__device__ __forceinline__ void load_pairs(F2* v, At at, In in) {
+  if constexpr (V == 1) {
+#pragma unroll
+    for (int i = 0; i < NV; i += 2) {
+      const float lo = in(i) ? to_f32<T>(*at(i)) : 0.0f;
+      const float hi = in(i + 1) ? to_f32<T>(*at(i + 1)) : 0.0f;
+      v[i / 2] = f2(lo, hi);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      Pack<T, V> r;
+      r.zero();
+      if (in(i)) r.load(at(i));
+#pragma unroll
+      for (int e = 0; e < V; e += 2) v[(i * V + e) / 2] = load_pair(&r.e[e]);
+    }
+  }
+}
+template <int V, int NV, typename At, typename In>
+__device__ __forceinline__ void store_pairs(const F2* v, At at, In in) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float o[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float2 f = f2_get(v[(i * V + e) / 2]);
+      o[e] = (i * V + e) % 2 ? f.y : f.x;
+    }
+    if (in(i)) store_f32<V>(at(i), o);
+  }
+}
+
+// kRowWarps: warps of a row; 0: p.row_warps (rows that are not whole vectors of four).
+template <typename T, int V, int E, int kThreads, int kRowWarps>
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
     layernorm_bwd_kernel(const LnBwdParams p) {
   using Shape = LnBwdShape<T, V, E, kThreads>;
   constexpr int NV = Shape::NV, kStages = Shape::kStages;
   extern __shared__ __align__(16) unsigned char ln_smem[];
   __shared__ float red[2][64];
-  const int warp = threadIdx.x >> 5, wr = warp % p.row_warps;
+  const int row_warps = kRowWarps ? kRowWarps : p.row_warps;
+  const int warp = threadIdx.x >> 5, wr = warp % row_warps;
   const int lane = threadIdx.x - (warp - wr) * 32;
-  const int tpr = p.row_warps * 32, rpb = blockDim.x / tpr;
+  const int tpr = row_warps * 32, rpb = kThreads / tpr;
   umma::grid_dep_wait();
 
-  float w[NV][V], dw[NV][V], db[NV][V];
+  // this thread's E columns: vector i starts at column col(i)
+  auto col = [&](int i) { return (i * tpr + lane) * V; };
+  auto in = [&](int i) { return col(i) < p.D; };
+  const F2 zero = f2(0.0f, 0.0f);
+  F2 w[E / 2], dw[E / 2], db[E / 2];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * tpr + lane) * V;
-#pragma unroll
-    for (int e = 0; e < V; ++e) w[i][e] = dw[i][e] = db[i][e] = 0.0f;
-    if (c < p.D) load_f32<V>(p.w + c, w[i]);
-  }
-  // vector i of array (0: x, 1: dy, 2: dresid) of this thread's row in a stage
+  for (int j = 0; j < E / 2; ++j) dw[j] = db[j] = zero;
+  load_pairs<float, V, NV>(w, [&](int i) { return p.w + col(i); }, in);
+  // vector i of an array (0: x, 1: dy, 2: dresid) of this thread's row in a stage
   auto slot = [&](int stage, int array, int i, long long row) -> unsigned char* {
     const int size = array == 2 ? Shape::kR : Shape::kX;
     if constexpr (Shape::kOwn) {
       return ln_smem + ((size_t)stage * Shape::kThread + array * NV * Shape::kX + i * size) * kThreads +
              threadIdx.x * size;
     } else {
-      return ln_smem + (size_t)(stage * rpb + warp / p.row_warps) * Shape::shared_row(p.D) +
+      return ln_smem + (size_t)(stage * rpb + warp / row_warps) * Shape::shared_row(p.D) +
              array * Shape::pieces(p.D * (int)sizeof(T)) +
              (array == 2 ? row_shift<float>(row, p.D) : row_shift<T>(row, p.D)) +
              (i * tpr + lane) * size;
@@ -246,19 +284,19 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 && E <= 16 ? 2 : 1)
   auto fetch = [&](long long row, int stage) {
     if (row < p.rows) {
       if constexpr (Shape::kOwn) {
-        const size_t off = (size_t)row * p.D;
+        const size_t off = (size_t)row * p.D + lane * V;
+        const T *fx = x + off, *fg = dy + off;
+        const float* fr = p.dresid + off;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          const int c = (i * tpr + lane) * V;
-          if (c < p.D) {
-            copy_async<Shape::kX>(slot(stage, 0, i, row), x + off + c);
-            copy_async<Shape::kX>(slot(stage, 1, i, row), dy + off + c);
-            if (p.dresid) copy_async<Shape::kR>(slot(stage, 2, i, row), p.dresid + off + c);
+          if (in(i)) {
+            copy_async<Shape::kX>(slot(stage, 0, i, row), fx + i * tpr * V);
+            copy_async<Shape::kX>(slot(stage, 1, i, row), fg + i * tpr * V);
+            if (p.dresid) copy_async<Shape::kR>(slot(stage, 2, i, row), fr + i * tpr * V);
           }
         }
       } else {
-        unsigned char* s =
-            ln_smem + (size_t)(stage * rpb + warp / p.row_warps) * Shape::shared_row(p.D);
+        unsigned char* s = ln_smem + (size_t)(stage * rpb + warp / row_warps) * Shape::shared_row(p.D);
         const int size = Shape::pieces(p.D * (int)sizeof(T));
         const long long n = p.rows * p.D;
         copy_row_pieces(s, x, row, p.D, n, lane, tpr);
@@ -270,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 && E <= 16 ? 2 : 1)
   };
   const float inv_d = 1.0f / p.D;
   const long long step = (long long)gridDim.x * rpb;
-  long long row = (long long)blockIdx.x * rpb + warp / p.row_warps;
+  long long row = (long long)blockIdx.x * rpb + warp / row_warps;
   if constexpr (Shape::kAhead) {
 #pragma unroll
     for (int k = 0; k < kStages - 1; ++k) fetch(row + k * step, k);
@@ -282,60 +320,54 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 && E <= 16 ? 2 : 1)
     const size_t off = (size_t)row * p.D;
     float next_mean = 0.0f, next_rstd = 0.0f;
     if (row + step < p.rows) next_mean = p.mean[row + step], next_rstd = p.rstd[row + step];
-    Pack<T, V> xv[NV], gv[NV];
+    F2 xh[E / 2], g[E / 2];
     if constexpr (Shape::kAhead) umma::cp_async_wait<kStages - 2>();
-    if constexpr (Shape::kShare) row_barrier(warp, p.row_warps);  // and the row before is done with
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * tpr + lane) * V;
-      xv[i].zero();
-      gv[i].zero();
-      if (c < p.D) {
-        if constexpr (Shape::kAhead) {
-          xv[i].load(reinterpret_cast<const T*>(slot(stage, 0, i, row)));
-          gv[i].load(reinterpret_cast<const T*>(slot(stage, 1, i, row)));
-        } else {
-          xv[i].load(x + off + c);
-          gv[i].load(dy + off + c);
-        }
-      }
-    }
+    if constexpr (Shape::kShare) row_barrier(warp, row_warps);  // and the row before is done with
+    auto input = [&](const T* from, int array) {
+      return [=](int i) {
+        if constexpr (Shape::kAhead) return reinterpret_cast<const T*>(slot(stage, array, i, row));
+        else return from + off + col(i);
+      };
+    };
+    load_pairs<T, V, NV>(xh, input(x, 0), in);
+    load_pairs<T, V, NV>(g, input(dy, 1), in);
     // into the slot of the row before
     if constexpr (Shape::kAhead)
       fetch(row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
-    float s[2] = {0.0f, 0.0f};
-    float xh[NV][V];
+    F2 s0 = zero, s1 = zero;
+    const F2 nm = f2(-mean, -mean), r2 = f2(rstd, rstd);
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float g = gv[i].get(e), t = g * w[i][e];
-        xh[i][e] = (xv[i].get(e) - mean) * rstd;
-        s[0] += t;
-        s[1] += t * xh[i][e];
-        dw[i][e] += g * xh[i][e];
-        db[i][e] += g;
-      }
-    row_sum<2>(s, red[buf], warp, wr, p.row_warps);
-    buf ^= 1;
-    const float c0 = s[0] * inv_d, c1 = s[1] * inv_d;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * tpr + lane) * V;
-      if (c < p.D) {
-        float o[V], d[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) d[e] = 0.0f;
-        if (p.dresid)
-          load_f32<V>(Shape::kAhead ? reinterpret_cast<const float*>(slot(stage, 2, i, row))
-                                    : p.dresid + off + c,
-                      d);
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-          o[e] = fmaf(rstd, gv[i].get(e) * w[i][e] - c0 - xh[i][e] * c1, d[e]);
-        store_f32<V>(p.dx + off + c, o);
-      }
+    for (int j = 0; j < E / 2; ++j) {
+      const F2 t = g[j] * w[j];
+      xh[j] = (xh[j] + nm) * r2;
+      s0 = s0 + t;
+      s1 = f2_fma(t, xh[j], s1);
+      dw[j] = f2_fma(g[j], xh[j], dw[j]);
+      db[j] = db[j] + g[j];
     }
+    float s[2] = {f2_get(s0).x + f2_get(s0).y, f2_get(s1).x + f2_get(s1).y};
+    row_sum<2>(s, red[buf], warp, wr, row_warps);
+    buf ^= 1;
+    const F2 c0 = f2(-s[0] * inv_d, -s[0] * inv_d), c1 = f2(-s[1] * inv_d, -s[1] * inv_d);
+#pragma unroll
+    for (int j = 0; j < E / 2; ++j)  // t - mean(t) - xh mean(t xh), times s below
+      g[j] = f2_fma(xh[j], c1, f2_fma(g[j], w[j], c0));
+    if (p.dresid) {
+      load_pairs<float, V, NV>(
+          xh,
+          [&](int i) {
+            if constexpr (Shape::kAhead) return reinterpret_cast<const float*>(slot(stage, 2, i, row));
+            else return p.dresid + off + col(i);
+          },
+          in);
+#pragma unroll
+      for (int j = 0; j < E / 2; ++j) g[j] = f2_fma(g[j], r2, xh[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < E / 2; ++j) g[j] = g[j] * r2;
+    }
+    float* dx = p.dx + off + lane * V;
+    store_pairs<V, NV>(g, [&](int i) { return dx + i * tpr * V; }, in);
     mean = next_mean;
     rstd = next_rstd;
     stage = stage + 1 == kStages ? 0 : stage + 1;
@@ -344,34 +376,22 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 && E <= 16 ? 2 : 1)
   // the groups of the CTA together, in order
   float* part = p.parts + (size_t)blockIdx.x * 2 * p.D;
   if (rpb == 1) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * tpr + lane) * V;
-      if (c < p.D) {
-        store_f32<V>(part + c, dw[i]);
-        store_f32<V>(part + p.D + c, db[i]);
-      }
-    }
+    store_pairs<V, NV>(dw, [&](int i) { return part + col(i); }, in);
+    store_pairs<V, NV>(db, [&](int i) { return part + p.D + col(i); }, in);
     return;
   }
   float* join = reinterpret_cast<float*>(ln_smem);  // [group][2][D]
-  float* own = join + (size_t)(warp / p.row_warps) * 2 * p.D;
+  float* own = join + (size_t)(warp / row_warps) * 2 * p.D;
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * tpr + lane) * V;
-    if (c < p.D) {
-      store_f32<V>(own + c, dw[i]);
-      store_f32<V>(own + p.D + c, db[i]);
-    }
-  }
+  store_pairs<V, NV>(dw, [&](int i) { return own + col(i); }, in);
+  store_pairs<V, NV>(db, [&](int i) { return own + p.D + col(i); }, in);
   __syncthreads();
 #pragma unroll 4
   for (int c = threadIdx.x * V; c < 2 * p.D; c += kThreads * V) {
     float s[V], o[V];
     load_f32<V>(join + c, s);
-    for (int g = 1; g < rpb; ++g) {
-      load_f32<V>(join + (size_t)g * 2 * p.D + c, o);
+    for (int k = 1; k < rpb; ++k) {
+      load_f32<V>(join + (size_t)k * 2 * p.D + c, o);
 #pragma unroll
       for (int e = 0; e < V; ++e) s[e] += o[e];
     }
