@@ -185,22 +185,28 @@ struct LnBwdShape {
   }
 };
 
-// The row of D values at element `row * D` of an array of n values, as 16-byte
-// pieces, into `to`, by the tpr threads of a group.
+// The row of D values at element `row * D` of an array of `rows` rows, as 16-byte
+// pieces, into `to`, by the tpr threads of a group.  Only the last row's pieces can
+// reach past the array.
 template <typename T>
 __device__ __forceinline__ void copy_row_pieces(unsigned char* to, const T* from, long long row,
-                                                int D, long long n, int lane, int tpr) {
-  const long long begin = row * D * (long long)sizeof(T), first = begin & ~15LL;
-  const int len = (int)(begin - first) + D * (int)sizeof(T);
-  const long long all = n * (long long)sizeof(T);
-  const unsigned char* src = reinterpret_cast<const unsigned char*>(from) + first;
-  for (int o = lane * 16; o < len; o += tpr * 16)
-    umma::cp_async16_part(to + o, src + o, (int)min(16LL, all - first - o));
+                                                int D, long long rows, int lane, int tpr) {
+  const long long begin = row * D * (long long)sizeof(T);
+  const int shift = (int)(begin & 15), len = shift + D * (int)sizeof(T);
+  const unsigned char* src = reinterpret_cast<const unsigned char*>(from) + (begin - shift) + lane * 16;
+  to += lane * 16;
+  if (row + 1 < rows) {
+    for (int o = lane * 16; o < len; o += tpr * 16, src += tpr * 16, to += tpr * 16)
+      umma::cp_async16(to, src, true);
+  } else {
+    for (int o = lane * 16; o < len; o += tpr * 16, src += tpr * 16, to += tpr * 16)
+      umma::cp_async16_part(to, src, min(16, len - o));
+  }
 }
 // Where the row's first value lies in its pieces.
 template <typename T>
 __device__ __forceinline__ int row_shift(long long row, int D) {
-  return (int)(row * D * (long long)sizeof(T) & 15);
+  return (int)((unsigned)row * (unsigned)D * (unsigned)sizeof(T) & 15u);  // low bits only
 }
 
 template <int Bytes>
@@ -268,17 +274,19 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
   for (int j = 0; j < E / 2; ++j) dw[j] = db[j] = zero;
   load_pairs<float, V, NV>(w, [&](int i) { return p.w + col(i); }, in);
   // vector i of an array (0: x, 1: dy, 2: dresid) of this thread's row in a stage
+  const int group = warp / row_warps, row_bytes = Shape::kShare ? Shape::shared_row(p.D) : 0,
+            array_bytes = Shape::pieces(p.D * (int)sizeof(T));
   auto slot = [&](int stage, int array, int i, long long row) -> unsigned char* {
     const int size = array == 2 ? Shape::kR : Shape::kX;
-    if constexpr (Shape::kOwn) {
-      return ln_smem + ((size_t)stage * Shape::kThread + array * NV * Shape::kX + i * size) * kThreads +
-             threadIdx.x * size;
-    } else {
-      return ln_smem + (size_t)(stage * rpb + warp / row_warps) * Shape::shared_row(p.D) +
-             array * Shape::pieces(p.D * (int)sizeof(T)) +
-             (array == 2 ? row_shift<float>(row, p.D) : row_shift<T>(row, p.D)) +
-             (i * tpr + lane) * size;
-    }
+    int at;
+    if constexpr (Shape::kOwn)
+      at = (stage * Shape::kThread + array * NV * Shape::kX + i * size) * kThreads +
+           (int)threadIdx.x * size;
+    else
+      at = (stage * rpb + group) * row_bytes + array * array_bytes +
+           (array == 2 ? row_shift<float>(row, p.D) : row_shift<T>(row, p.D)) +
+           (i * tpr + lane) * size;
+    return ln_smem + at;
   };
   const T *x = static_cast<const T*>(p.x), *dy = static_cast<const T*>(p.dy);
   auto fetch = [&](long long row, int stage) {
@@ -296,19 +304,17 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
           }
         }
       } else {
-        unsigned char* s = ln_smem + (size_t)(stage * rpb + warp / row_warps) * Shape::shared_row(p.D);
-        const int size = Shape::pieces(p.D * (int)sizeof(T));
-        const long long n = p.rows * p.D;
-        copy_row_pieces(s, x, row, p.D, n, lane, tpr);
-        copy_row_pieces(s + size, dy, row, p.D, n, lane, tpr);
-        if (p.dresid) copy_row_pieces(s + 2 * size, p.dresid, row, p.D, n, lane, tpr);
+        unsigned char* s = ln_smem + (stage * rpb + group) * row_bytes;
+        copy_row_pieces(s, x, row, p.D, p.rows, lane, tpr);
+        copy_row_pieces(s + array_bytes, dy, row, p.D, p.rows, lane, tpr);
+        if (p.dresid) copy_row_pieces(s + 2 * array_bytes, p.dresid, row, p.D, p.rows, lane, tpr);
       }
     }
     umma::cp_async_commit();
   };
   const float inv_d = 1.0f / p.D;
   const long long step = (long long)gridDim.x * rpb;
-  long long row = (long long)blockIdx.x * rpb + warp / row_warps;
+  long long row = (long long)blockIdx.x * rpb + group;
   if constexpr (Shape::kAhead) {
 #pragma unroll
     for (int k = 0; k < kStages - 1; ++k) fetch(row + k * step, k);
@@ -381,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
     return;
   }
   float* join = reinterpret_cast<float*>(ln_smem);  // [group][2][D]
-  float* own = join + (size_t)(warp / row_warps) * 2 * p.D;
+  float* own = join + group * 2 * p.D;
   __syncthreads();
   store_pairs<V, NV>(dw, [&](int i) { return own + col(i); }, in);
   store_pairs<V, NV>(db, [&](int i) { return own + p.D + col(i); }, in);
@@ -391,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
     float s[V], o[V];
     load_f32<V>(join + c, s);
     for (int k = 1; k < rpb; ++k) {
-      load_f32<V>(join + (size_t)k * 2 * p.D + c, o);
+      load_f32<V>(join + k * 2 * p.D + c, o);
 #pragma unroll
       for (int e = 0; e < V; ++e) s[e] += o[e];
     }
