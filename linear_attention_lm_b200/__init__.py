@@ -493,9 +493,12 @@ def based_baseconv_fwd(x, w, bias, taps, y, stream=None):
 def _need(t, shape, dtype, name: str, device: torch.device, index: int):
     """Pointer of a tensor that must have exactly this shape and dtype, be
     contiguous and sit on this device (index: the device's)."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
-            and t.shape == shape and t.is_contiguous()):
-        return t.data_ptr() or None
+    try:
+        if (t.shape == shape and t.dtype is dtype and t.get_device() == index
+                and t.is_contiguous()):
+            return t.data_ptr() or None
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.shape != shape:
@@ -512,24 +515,36 @@ def _may(t, shape, dtype, name: str, device: torch.device, index: int):
     return None if t is None else _need(t, shape, dtype, name, device, index)
 
 
-# the current stream's handle without a stream object around it
+# the current stream's handle without a stream object around it, and the current device
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _place(x):
+    """Device, its index and the dtype code of the tensor that the sizes come from."""
+    try:
+        index, dtype = x.get_device(), x.dtype
+    except AttributeError:
+        raise TypeError("expected a torch.Tensor") from None
+    if index < 0:
+        raise ValueError("tensors must live on a CUDA device")
+    return x.device, index, BASED_BF16 if dtype is torch.bfloat16 else _dtype_code(x)
 
 
 def _run(fn: str, args, stream, device: torch.device):
     """Call an entry point whose last argument is the stream, with the tensors'
     device current (these calls can be as short as their launch: nothing is
     switched or wrapped that need not be)."""
-    if isinstance(stream, torch.cuda.Stream):
+    index = device.index
+    if stream is None:
+        handle = (_current_raw_stream(index) if _current_raw_stream is not None
+                  else torch.cuda.current_stream(device).cuda_stream)
+    elif isinstance(stream, torch.cuda.Stream):
         handle = stream.cuda_stream
-    elif stream is not None:
-        handle = int(stream)
-    elif _current_raw_stream is not None:
-        handle = _current_raw_stream(device.index)
     else:
-        handle = torch.cuda.current_stream(device).cuda_stream
+        handle = int(stream)
     call = getattr(_lib or load_library(), fn)
-    if torch.cuda.current_device() == device.index:
+    if _current_device() == index:
         st = call(*args, handle)
     else:
         with torch.cuda.device(device):
@@ -543,11 +558,10 @@ def based_layernorm_fwd(x, weight, bias, y, eps: float = 1e-5, residual=None, re
     """y = layer norm of r = x (+ residual) over the last axis, times weight
     (+ bias).  x, y, residual, resid_out [..., D]; weight, bias [D] float32; mean,
     rstd float32 of x's leading shape (written if given, for the gradient)."""
-    dev = _cuda(_device_of(x))
-    if x.dim() < 1:
+    dev, at, dt = _place(x)
+    shape, dtype, f32 = x.shape, x.dtype, torch.float32
+    if not shape:
         raise ValueError("x must be [..., D]")
-    shape, dtype, f32, at = x.shape, x.dtype, torch.float32, dev.index
-    dt = _dtype_code(x)
     lead, row = shape[:-1], shape[-1:]
     if (residual is None) != (resid_out is None):
         raise ValueError("residual and resid_out are given together")
@@ -573,11 +587,10 @@ def based_layernorm_bwd(dy, x, weight, mean, rstd, dx, dweight, dbias, dresid=No
     """Gradients (float32, written) of based_layernorm_fwd: dx [..., D] (with
     dresid added, the gradient that reaches the residual stream from elsewhere),
     dweight, dbias [D].  x is the normalised stream (resid_out, or x)."""
-    dev = _cuda(_device_of(x))
-    if x.dim() < 1:
+    dev, at, dt = _place(x)
+    shape, dtype, f32 = x.shape, x.dtype, torch.float32
+    if not shape:
         raise ValueError("x must be [..., D]")
-    shape, dtype, f32, at = x.shape, x.dtype, torch.float32, dev.index
-    dt = _dtype_code(x)
     lead, row = shape[:-1], shape[-1:]
     rows, D = lead.numel(), row[0]
     args = (_need(dy, shape, dtype, "dy", dev, at), _need(x, shape, dtype, "x", dev, at),
@@ -622,23 +635,22 @@ def _shape_of(t, name: str):
 
 def _rotary(fn, q, k, q_out, k_out, freqs, pos, layout, mscale, dtype, stream):
     ref = q if q is not None else k
-    dev = _cuda(_device_of(ref))
+    dev, at, dt = _place(ref)
     if (q is None) != (q_out is None) or (k is None) != (k_out is None):
         raise ValueError("q and q_out, k and k_out are given together")
-    if ref.dim() != 4:
+    shape = ref.shape
+    if len(shape) != 4:
         raise ValueError("q, k must be [B, H, L, d_head]")
     if layout not in ROTARY_LAYOUTS:
         raise ValueError(f"layout: one of {sorted(ROTARY_LAYOUTS)}, got {layout!r}")
-    shape = ref.shape
     B, _, L, D = shape
     k_shape = None if k is None else _shape_of(k, "k")
     if k_shape is not None and (len(k_shape) != 4 or k_shape[0] != B or k_shape[2:] != shape[2:]):
         raise ValueError(f"k: expected shape {(B, 'H', L, D)}, got {tuple(k_shape)}")
     dtype = dtype or ref.dtype
-    dt = _dtype_code(ref)
-    if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
-        raise TypeError("freqs must be a float64 tensor [rot_dim / 2]")
-    f_shape, at = freqs.shape, dev.index
+    f_shape = _shape_of(freqs, "freqs")
+    if len(f_shape) != 1:
+        raise ValueError(f"freqs: expected shape [rot_dim / 2], got {tuple(f_shape)}")
     per_seq = isinstance(pos, torch.Tensor)
     args = (_may(q, shape, dtype, "q", dev, at), _may(k, k_shape, dtype, "k", dev, at),
             _may(q_out, shape, dtype, "q_out", dev, at), _may(k_out, k_shape, dtype, "k_out", dev, at),
@@ -674,12 +686,12 @@ GATEDREC_CHUNK = 64
 
 
 def _gatedrec_args(x):
-    dev = _cuda(_device_of(x))
+    dev, at, dt = _place(x)
     shape = x.shape
     if len(shape) != 3:
         raise ValueError("x, g must be [B, L, D]")
     B, L, D = shape
-    return dev, dev.index, shape, x.dtype, (B, D), (B, -(-L // GATEDREC_CHUNK), D), _dtype_code(x)
+    return dev, at, shape, x.dtype, (B, D), (B, -(-L // GATEDREC_CHUNK), D), dt
 
 
 def based_gatedrec_fwd(x, g, y, h0=None, h_last=None, h_chunks=None, lengths=None, stream=None):
@@ -714,14 +726,14 @@ def based_gatedrec_bwd(x, g, dy, h_chunks, dx, dg, dh_last=None, dh0=None, lengt
 
 def based_gatedrec_step(x, g, h, y, stream=None):
     """One token: h [B, D] float32 becomes a h + (1 - a) x (in place), y [B, D] = h."""
-    dev = _cuda(_device_of(x))
-    shape, dtype, at = x.shape, x.dtype, dev.index
+    dev, at, dt = _place(x)
+    shape, dtype = x.shape, x.dtype
     if len(shape) != 2:
         raise ValueError("x, g must be [B, D]")
     _run("based_gatedrec_step",
          (_need(x, shape, dtype, "x", dev, at), _need(g, shape, dtype, "g", dev, at),
           _need(h, shape, torch.float32, "h", dev, at), _need(y, shape, dtype, "y", dev, at),
-          *shape, _dtype_code(x)), stream, dev)
+          *shape, dt), stream, dev)
     return y
 
 
