@@ -373,7 +373,8 @@ based_status_t based_rotary_freqs(double* freqs, int rot_dim, double base,
  *   freqs    [rot_dim/2] fp64, DEVICE memory, turns per position (see above)
  *   pos      DEVICE array of B int64 (8-byte aligned): token t of sequence b is
  *            at position pos[b] + t; NULL: at pos0 + t for every sequence
- * 2 <= rot_dim <= D, even.  Positions lie in [0, 2^31): pos0 outside is refused
+ * 2 <= rot_dim <= D <= 65536, even, H_q + H_k <= 2^19 (else BASED_ERR_UNSUPPORTED
+ * for the upper limits, BASED_ERR_INVALID_ARG for the others).  Positions lie in [0, 2^31): pos0 outside is refused
  * (negative: BASED_ERR_INVALID_ARG, too large: BASED_ERR_UNSUPPORTED); an entry of
  * pos outside is found by the kernel, which leaves that sequence's outputs
  * untouched and records BASED_ERR_INVALID_ARG (based_get_device_error).
@@ -416,7 +417,8 @@ based_status_t based_rotary_bwd(const float* dq_out, const float* dk_out, float*
  *             h_chunks are written as zero there.  An entry outside [0, L] is found
  *             by the kernel: that sequence's outputs are left untouched and
  *             BASED_ERR_INVALID_ARG is recorded (based_get_device_error).
- * The state is fp32 throughout.  L = 0: h_last = h0.
+ * The state is fp32 throughout.  L = 0: h_last = h0.  D <= 2^20 (else
+ * BASED_ERR_UNSUPPORTED).
  */
 based_status_t based_gatedrec_fwd(const void* x, const void* g, void* y, const float* h0,
                                   float* h_last, float* h_chunks, const long long* lengths, int B,

@@ -10,7 +10,6 @@
 namespace {
 
 inline bool dtype_ok(based_dtype_t dt) { return dt == BASED_F32 || dt == BASED_BF16; }
-inline int dtype_bytes(based_dtype_t dt) { return dt == BASED_F32 ? 4 : 2; }
 inline long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
 // Runs f(T{}, integral_constant<V>) for the type and the widest vector of at
@@ -180,13 +179,15 @@ based_status_t rotary_impl(const void* q, const void* k, void* q_out, void* k_ou
     return BASED_ERR_INVALID_ARG;
   if (!pos && pos0 < 0) return BASED_ERR_INVALID_ARG;
   if (!pos && pos0 > (1LL << 31) - L) return BASED_ERR_UNSUPPORTED;
-  const bool no_q = (long long)B * H_q * L == 0, no_k = (long long)B * H_k * L == 0;
+  const bool no_q = B == 0 || H_q == 0 || L == 0, no_k = B == 0 || H_k == 0 || L == 0;
   based_status_t s;
   if ((s = check_tensor(q, no_q)) != BASED_OK) return s;
   if ((s = check_tensor(q_out, no_q)) != BASED_OK) return s;
   if ((s = check_tensor(k, no_k)) != BASED_OK) return s;
   if ((s = check_tensor(k_out, no_k)) != BASED_OK) return s;
   if (no_q && no_k) return BASED_OK;
+  if ((long long)B * L > (1LL << 40) || (long long)H_q + H_k > (1 << 19) || D > (1 << 16))
+    return BASED_ERR_UNSUPPORTED;
   if (!freqs || (reinterpret_cast<uintptr_t>(freqs) & 7u) ||
       (reinterpret_cast<uintptr_t>(pos) & 7u))
     return BASED_ERR_INVALID_ARG;

@@ -166,8 +166,8 @@ struct LnBwdParams {
 // copied ahead by cp.async.  Where rows are whole vectors of four, each thread
 // copies what it will read itself and no barrier is between a row's arrival and its
 // use; other rows are copied as the 16-byte pieces that hold them, by the whole
-// group (3001 x 999 fp32: 19.8 us with 4-byte copies, 18.2 with pieces; 16384 x 999 bf16, where
-// two-byte copies have no asynchronous form: 148 and 72 us).
+// group (3001 x 999 fp32: 19.8 us with 4-byte copies, 15.3 with pieces; 16384 x 999
+// bf16, where two-byte copies have no asynchronous form: 148 and 59 us).
 template <typename T, int V, int E, int kThreads>
 struct LnBwdShape {
   static constexpr int NV = E / V;

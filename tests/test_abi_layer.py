@@ -86,7 +86,9 @@ def test_rotary_refusals(lib):
                dict(f=N), dict(q=FAKE + 2), dict(ko=FAKE + 8), dict(f=FAKE + 4),
                dict(pos=FAKE + 4)):
         assert rot(lib, **kw) == INVALID, kw
-    assert rot(lib, pos0=(1 << 31) - 7) == UNSUPPORTED
+    for kw in (dict(pos0=(1 << 31) - 7), dict(D=65538), dict(Hq=1 << 19), dict(B=1 << 21, L=1 << 21),
+               dict(Hq=(1 << 31) - 1, Hk=(1 << 31) - 1)):
+        assert rot(lib, **kw) == UNSUPPORTED, kw
     assert rot(lib, q=N, k=N, qo=N, ko=N, f=N, L=0) == OK
     assert rot(lib, q=N, k=N, qo=N, ko=N, f=N, Hq=0, Hk=0) == OK
     f = lib.based_rotary_bwd
@@ -139,6 +141,7 @@ def test_gatedrec_refusals(lib):
         assert f(lib, x=N, g=N, L=0, **({"y": N} if f is rec else
                                         dict(dy=N, hc=N, dx=N, dg=N))) == OK
         assert f(lib, B=1 << 30, L=0, D=1 << 20) == UNSUPPORTED
+        assert f(lib, D=(1 << 20) + 1) == UNSUPPORTED
     for kw in (dict(y=N), dict(h0=FAKE + 4), dict(hl=FAKE + 4), dict(hc=FAKE + 4)):
         assert rec(lib, **kw) == INVALID, kw
     for kw in (dict(dy=N), dict(hc=N), dict(dx=N), dict(dg=N), dict(dhl=FAKE + 4),
