@@ -227,7 +227,7 @@ __device__ __forceinline__ void gr_fetch(T* slot, const T* src, int D, int t0, i
     else if constexpr (CW >= 4) umma::cp_async_small<CW>(to, from, in);
     else *to = in ? *from : from_f32<T>(0.0f);
   };
-  if constexpr (CW == 16) {  // every token inside: a start and constant steps
+  if constexpr (CW >= 4 && RC <= 32) {  // every token inside: a start and constant steps
     constexpr int R = 32 / RC;  // rows per copy instruction
     static_assert(RC <= 32 && (S % R == 0 || R % S == 0), "the step of a row is a constant");
     if (t0 + G * S <= end) {
@@ -408,13 +408,14 @@ struct GrBwdParams {
 
 template <typename T, int G>
 struct GrBwdShape {
-  static constexpr int S = 8;
+  static constexpr int S = 16 / (int)sizeof(T);  // a ring slot of x, g and dy: 3 KiB per warp
   static constexpr int kTile = S * G * kGrWarps;
   static constexpr int kSlot = 3 * S * 64;
-  static_assert(kTile % kGrChunk == 0, "the forward states of a tile start from a saved state");
   static constexpr size_t kShared = sizeof(GrShared) + sizeof(ulonglong2) * 2 * kGrWarps * 32;
   static constexpr size_t kSmem = kShared + sizeof(T) * kGrWarps * kGrStages * kSlot;
 };
+template <typename T>
+constexpr int kGrBwdMinG = sizeof(T) == 2 ? 1 : 2;  // whole chunks
 
 // The same cut, walked from the end.  The state that enters a tile is the saved
 // one, so the forward maps only have to meet inside the CTA; the gradient's maps
@@ -423,6 +424,7 @@ template <typename T, int G, int CW>
 __global__ void __launch_bounds__(kGrThreads, 2) gatedrec_bwd_kernel(const GrBwdParams p) {
   using Shape = GrBwdShape<T, G>;
   constexpr int S = Shape::S, kTile = Shape::kTile, kCols = 64 / G;
+  static_assert(kTile % kGrChunk == 0, "the forward states of a tile start from a saved state");
   constexpr bool kPair = CW > (int)sizeof(T);
   extern __shared__ __align__(16) unsigned char gr_smem[];
   GrShared& sh = *reinterpret_cast<GrShared*>(gr_smem);
@@ -547,6 +549,173 @@ __global__ void __launch_bounds__(kGrThreads, 2) gatedrec_bwd_kernel(const GrBwd
   if (p.dh0) {
     if (live && rank == 0 && w == 0 && grp == 0) gr_store<kPair>(p.dh0 + (size_t)b * p.D + c, l, two);
   }
+}
+
+// Short sequences, or very many: a thread walks one sequence's two channels from
+// end to end, the next kGrBatch tokens in flight.
+constexpr int kGrShortThreads = 128, kGrBatch = 8;
+static_assert(kGrChunk % kGrBatch == 0, "chunks start with a batch");
+
+template <typename T, bool kPair>
+struct GrWalk {
+  int b, c, len;
+  bool live, two;
+  size_t seq;
+  __device__ __forceinline__ GrWalk(const long long* lengths, int B, int L, int D) {
+    const int pairs = (D + 1) / 2;
+    const long long i = (long long)blockIdx.x * kGrShortThreads + threadIdx.x;
+    live = i < (long long)B * pairs;
+    b = live ? (int)(i / pairs) : 0;
+    c = live ? (int)(i % pairs) * 2 : 0;
+    two = c + 1 < D;
+    len = L;
+    if (lengths && live) {
+      const long long n = lengths[b];
+      if (n < 0 || n > L) {
+        if (c == 0) record_device_error(BASED_ERR_INVALID_ARG);
+        live = false;
+      } else {
+        len = (int)n;
+      }
+    }
+    seq = (size_t)b * L * D + c;
+  }
+  // two channels of tensor p, `at` values on, as they lie in memory
+  __device__ __forceinline__ void get(Pack<T, 2>& v, const void* p, size_t at) const {
+    const T* q = static_cast<const T*>(p) + seq + at;
+    if constexpr (kPair) {
+      v.load(q);
+    } else {
+      v.e[0] = q[0];
+      v.e[1] = two ? q[1] : q[0];
+    }
+  }
+};
+template <typename T>
+__device__ __forceinline__ F2 to_pair(const Pack<T, 2>& v) { return load_pair(&v.e[0]); }
+
+template <typename T, bool kPair>
+__global__ void __launch_bounds__(kGrShortThreads) gatedrec_short_fwd_kernel(const GrFwdParams p,
+                                                                             int B) {
+  umma::grid_dep_wait();
+  const GrWalk<T, kPair> k(p.lengths, B, p.L, p.D);
+  if (!k.live) return;
+  const size_t state = (size_t)k.b * p.D + k.c;
+  const F2 zero = f2(0.0f, 0.0f);
+  F2 h = p.h0 ? gr_load<kPair>(p.h0 + state, k.two) : zero;
+  const int n_chunks = (p.L + kGrChunk - 1) / kGrChunk;
+  float* chunk = p.h_chunks ? p.h_chunks + (size_t)k.b * n_chunks * p.D + k.c : nullptr;
+  T* y = static_cast<T*>(p.y) + k.seq;
+  Pack<T, 2> x[kGrBatch], g[kGrBatch];
+  auto fetch = [&](int t0) {
+#pragma unroll
+    for (int s = 0; s < kGrBatch; ++s)
+      if (t0 + s < k.len) {
+        k.get(x[s], p.x, (size_t)(t0 + s) * p.D);
+        k.get(g[s], p.g, (size_t)(t0 + s) * p.D);
+      }
+  };
+  fetch(0);
+  for (int t0 = 0; t0 < p.L; t0 += kGrBatch) {
+    if (chunk && t0 % kGrChunk == 0) {
+      gr_store<kPair>(chunk, t0 < k.len ? h : zero, k.two);
+      chunk += p.D;
+    }
+    F2 a[kGrBatch], u[kGrBatch];
+#pragma unroll
+    for (int s = 0; s < kGrBatch; ++s) {
+      const Gate2 gt = gate_of(to_pair(g[s]));
+      a[s] = gt.a;
+      u[s] = gt.n * to_pair(x[s]);
+    }
+    fetch(t0 + kGrBatch);
+#pragma unroll
+    for (int s = 0; s < kGrBatch; ++s)
+      if (t0 + s < p.L) {
+        if (t0 + s < k.len) h = f2_fma(a[s], h, u[s]);
+        gr_store<kPair>(y + (size_t)(t0 + s) * p.D, t0 + s < k.len ? h : zero, k.two);
+      }
+  }
+  if (p.h_last) gr_store<kPair>(p.h_last + state, h, k.two);
+}
+
+// Dynamic shared memory: the state that enters each token, [L][threads] pairs.
+template <typename T, bool kPair>
+__global__ void __launch_bounds__(kGrShortThreads) gatedrec_short_bwd_kernel(const GrBwdParams p,
+                                                                             int B) {
+  extern __shared__ __align__(16) unsigned char gr_smem[];
+  F2* before = reinterpret_cast<F2*>(gr_smem) + threadIdx.x;
+  umma::grid_dep_wait();
+  const GrWalk<T, kPair> k(p.lengths, B, p.L, p.D);
+  if (!k.live) return;
+  const size_t state = (size_t)k.b * p.D + k.c;
+  const F2 zero = f2(0.0f, 0.0f), minus = f2(-1.0f, -1.0f);
+  F2 h = k.len > 0 ? gr_load<kPair>(p.h_chunks + state, k.two) : zero;
+  Pack<T, 2> x[kGrBatch], g[kGrBatch], d[kGrBatch];
+  auto fetch = [&](int t0) {
+#pragma unroll
+    for (int s = 0; s < kGrBatch; ++s)
+      if (t0 + s < k.len) {
+        k.get(x[s], p.x, (size_t)(t0 + s) * p.D);
+        k.get(g[s], p.g, (size_t)(t0 + s) * p.D);
+      }
+  };
+  fetch(0);
+  for (int t0 = 0; t0 < k.len; t0 += kGrBatch) {
+    F2 a[kGrBatch], u[kGrBatch];
+#pragma unroll
+    for (int s = 0; s < kGrBatch; ++s) {
+      const Gate2 gt = gate_of(to_pair(g[s]));
+      a[s] = gt.a;
+      u[s] = gt.n * to_pair(x[s]);
+    }
+    fetch(t0 + kGrBatch);
+#pragma unroll
+    for (int s = 0; s < kGrBatch; ++s)
+      if (t0 + s < k.len) {
+        before[(t0 + s) * kGrShortThreads] = h;
+        h = f2_fma(a[s], h, u[s]);
+      }
+  }
+  F2 l = p.dh_last ? gr_load<kPair>(p.dh_last + state, k.two) : zero;
+  float *dx = p.dx + k.seq, *dg = p.dg + k.seq;
+  for (int t = p.L - 1; t >= k.len; --t) {
+    gr_store<kPair>(dx + (size_t)t * p.D, zero, k.two);
+    gr_store<kPair>(dg + (size_t)t * p.D, zero, k.two);
+  }
+  auto fetch_back = [&](int t1) {  // tokens t1 - 1, t1 - 2, ...
+#pragma unroll
+    for (int s = 0; s < kGrBatch; ++s)
+      if (t1 - 1 - s >= 0) {
+        const size_t at = (size_t)(t1 - 1 - s) * p.D;
+        k.get(x[s], p.x, at);
+        k.get(g[s], p.g, at);
+        k.get(d[s], p.dy, at);
+      }
+  };
+  fetch_back(k.len);
+  for (int t1 = k.len; t1 > 0; t1 -= kGrBatch) {
+    F2 a[kGrBatch], n[kGrBatch], dv[kGrBatch], diff[kGrBatch];
+#pragma unroll
+    for (int s = 0; s < kGrBatch; ++s) {
+      const Gate2 gt = gate_of(to_pair(g[s]));
+      a[s] = gt.a;
+      n[s] = gt.n;
+      dv[s] = to_pair(d[s]);
+      diff[s] = f2_fma(to_pair(x[s]), minus, before[max(t1 - 1 - s, 0) * kGrShortThreads]);
+    }
+    fetch_back(t1 - kGrBatch);
+#pragma unroll
+    for (int s = 0; s < kGrBatch; ++s)
+      if (t1 - 1 - s >= 0) {
+        const size_t at = (size_t)(t1 - 1 - s) * p.D;
+        const F2 lt = l + dv[s], dxv = n[s] * lt;
+        l = a[s] * lt;
+        gr_store<kPair>(dx + at, dxv, k.two);
+        gr_store<kPair>(dg + at, dxv * diff[s] * a[s], k.two);
+      }
+  }
+  if (p.dh0) gr_store<kPair>(p.dh0 + state, l, k.two);
 }
 
 // One token: h = a h + (1 - a) x in place, y = round_dt(h).

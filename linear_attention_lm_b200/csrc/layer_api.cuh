@@ -257,7 +257,7 @@ bool launch_gatedrec(void (*kern)(P), const P& p, long long clusters, size_t sme
 struct GrPlan {
   int G, N, n_blk;
 };
-inline GrPlan plan_gatedrec(int B, int L, int D, int group_tokens, bool padded) {
+inline GrPlan plan_gatedrec(int B, int L, int D, int group_tokens, bool padded, int min_g) {
   const long long slots = (padded && B > 1 ? 4LL : 2LL) * device_sm_count();
   auto cut = [&](int G) {
     GrPlan pl{G, 1, (int)ceil_div(D, 64 / G)};
@@ -269,10 +269,34 @@ inline GrPlan plan_gatedrec(int B, int L, int D, int group_tokens, bool padded) 
   auto more = [&](int G) {
     return B * ceil_div(D, 64 / G) <= slots && (long long)G / 2 * kGrWarps * group_tokens < L;
   };
-  GrPlan pl = cut(1);
-  if (more(2)) pl = cut(2);
+  GrPlan pl = cut(min_g);
+  if (pl.G == 1 && more(2)) pl = cut(2);
   if (pl.G == 2 && more(4) && (padded || (long long)B * pl.n_blk * pl.N * 2 <= slots)) pl = cut(4);
   return pl;
+}
+
+// Whether one thread per two channels walks the sequences: they are shorter than
+// a round of tiles, or so many that the walk fills the GPU.  128 x L x 1024 bf16,
+// forward, walked and in tiles: L = 16 under 10 and 26.8 us, 64: 14.6 and 26.5,
+// 128: 27.0 and 30.1 (64 x 256 x 1024: 39.8 and 24.8); gradient: L = 16 under 9 and
+// 25.2, 48: 22.7 and 30.6, 64: 41.9 and 34.2.  Odd rows, with single loads, lose
+// beyond the shortest (128 x 128 x 999: 112 and 64 us).
+inline bool gatedrec_short(int B, int L, int D, bool forward) {
+  if (L <= 16) return true;
+  if (D % 2 != 0) return false;
+  const long long per_sm = (long long)B * D / device_sm_count();
+  return per_sm >= 128 && L <= (forward ? (per_sm >= 800 ? 128 : 64) : 48);
+}
+template <typename P>
+based_status_t launch_gatedrec_short(void (*pair)(P, int), void (*single)(P, int), const P& p, int B,
+                                     size_t smem, cudaStream_t st) {
+  auto kern = p.D % 2 == 0 ? pair : single;
+  const long long blocks = ceil_div((long long)B * ((p.D + 1) / 2), kGrShortThreads);
+  if (blocks > 0x7fffffffLL) return BASED_ERR_UNSUPPORTED;
+  if (!set_smem(kern, smem) ||
+      !launch_dependent(kern, dim3((unsigned)blocks), dim3(kGrShortThreads), smem, st, p, B))
+    return BASED_ERR_CUDA;
+  return launch_status();
 }
 
 }  // namespace
@@ -397,10 +421,19 @@ based_status_t based_gatedrec_fwd(const void* x, const void* g, void* y, const f
   GrFwdParams p{};
   p.x = x; p.g = g; p.y = y; p.h0 = h0; p.h_last = h_last; p.h_chunks = h_chunks;
   p.lengths = lengths; p.L = L; p.D = D;
+  if (gatedrec_short(B, L, D, true)) {
+    const size_t smem = 0;
+    return dt == BASED_F32
+               ? launch_gatedrec_short(gatedrec_short_fwd_kernel<float, true>,
+                                       gatedrec_short_fwd_kernel<float, false>, p, B, smem, st)
+               : launch_gatedrec_short(gatedrec_short_fwd_kernel<__nv_bfloat16, true>,
+                                       gatedrec_short_fwd_kernel<__nv_bfloat16, false>, p, B, smem,
+                                       st);
+  }
   return for_copies(dt, D, [&](auto t, auto cw) -> based_status_t {
     using T = decltype(t);
     constexpr int CW = decltype(cw)::value;
-    const GrPlan pl = plan_gatedrec(B, L, D, GrFwdShape<T, 1>::S, lengths != nullptr);
+    const GrPlan pl = plan_gatedrec(B, L, D, GrFwdShape<T, 1>::S, lengths != nullptr, 1);
     p.n_blk = pl.n_blk;
     p.N = pl.N;
     const long long clusters = (long long)B * pl.n_blk;
@@ -429,17 +462,33 @@ based_status_t based_gatedrec_bwd(const void* x, const void* g, const void* dy,
   GrBwdParams p{};
   p.x = x; p.g = g; p.dy = dy; p.h_chunks = h_chunks; p.dh_last = dh_last;
   p.dx = dx; p.dg = dg; p.dh0 = dh0; p.lengths = lengths; p.L = L; p.D = D;
+  if (gatedrec_short(B, L, D, false)) {
+    const size_t smem = sizeof(F2) * kGrShortThreads * (size_t)L;
+    return dt == BASED_F32
+               ? launch_gatedrec_short(gatedrec_short_bwd_kernel<float, true>,
+                                       gatedrec_short_bwd_kernel<float, false>, p, B, smem, st)
+               : launch_gatedrec_short(gatedrec_short_bwd_kernel<__nv_bfloat16, true>,
+                                       gatedrec_short_bwd_kernel<__nv_bfloat16, false>, p, B, smem,
+                                       st);
+  }
   return for_copies(dt, D, [&](auto t, auto cw) -> based_status_t {
     using T = decltype(t);
     constexpr int CW = decltype(cw)::value;
-    const GrPlan pl = plan_gatedrec(B, L, D, GrBwdShape<T, 1>::S, lengths != nullptr);
+    const GrPlan pl = plan_gatedrec(B, L, D, GrBwdShape<T, 1>::S, lengths != nullptr,
+                                    kGrBwdMinG<T>);
     p.n_blk = pl.n_blk;
     p.N = pl.N;
     const long long clusters = (long long)B * pl.n_blk;
     const size_t smem = GrBwdShape<T, 1>::kSmem;  // the same for every G
-    const bool ok = pl.G == 1   ? launch_gatedrec(gatedrec_bwd_kernel<T, 1, CW>, p, clusters, smem, st)
-                    : pl.G == 2 ? launch_gatedrec(gatedrec_bwd_kernel<T, 2, CW>, p, clusters, smem, st)
-                                : launch_gatedrec(gatedrec_bwd_kernel<T, 4, CW>, p, clusters, smem, st);
+    if constexpr (kGrBwdMinG<T> == 1) {
+      if (pl.G == 1) {
+        if (!launch_gatedrec(gatedrec_bwd_kernel<T, 1, CW>, p, clusters, smem, st))
+          return BASED_ERR_CUDA;
+        return launch_status();
+      }
+    }
+    const bool ok = pl.G == 2 ? launch_gatedrec(gatedrec_bwd_kernel<T, 2, CW>, p, clusters, smem, st)
+                              : launch_gatedrec(gatedrec_bwd_kernel<T, 4, CW>, p, clusters, smem, st);
     if (!ok) return BASED_ERR_CUDA;
     return launch_status();
   });

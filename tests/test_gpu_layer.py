@@ -331,7 +331,8 @@ def rec_bounds(x, g, h0, dy=None, dh=None, lengths=None):
 
 REC_SIZES = [(1, 1, 1), (3, 2, 33), (2, 63, 64), (1, 64, 100), (2, 65, 1000), (4, 130, 256),
              (1, 700, 40), (1, 1025, 1024), (2, 257, 2050), (5, 31, 8), (1, 4100, 72), (40, 20, 64),
-             (3, 3000, 24)]
+             (3, 3000, 24), (128, 40, 256), (150, 64, 130), (130, 17, 151), (9, 16, 21),
+             (240, 100, 500)]
 
 
 def rec_inputs(B, L, D, dtype, ragged):
@@ -450,19 +451,20 @@ def test_gatedrec_empty():
     assert torch.equal(dh0, h0)
 
 
-def test_gatedrec_length_out_of_range():
-    x, g = gen(1, (4, 70, 96), "bf16"), gen(2, (4, 70, 96), "bf16")
-    n = torch.tensor([70, 71, -1, 33], device="cuda")
+@pytest.mark.parametrize("L", [70, 14])
+def test_gatedrec_length_out_of_range(L):
+    x, g = gen(1, (4, L, 96), "bf16"), gen(2, (4, L, 96), "bf16")
+    n = torch.tensor([L, L + 1, -1, L // 2], device="cuda")
     y, last = torch.full_like(x, 77.0), torch.full((4, 96), 77.0, device="cuda")
-    chunks = torch.full((4, 2, 96), 77.0, device="cuda")
+    chunks = torch.full((4, -(-L // 64), 96), 77.0, device="cuda")
     lab.based_gatedrec_fwd(x, g, y, None, last, chunks, n)
     assert lab.based_get_device_error() == 1
     assert bool((y[1:3] == 77).all() and (last[1:3] == 77).all() and (chunks[1:3] == 77).all())
-    ok = torch.tensor([70, 0, 0, 33], device="cuda")
+    ok = torch.tensor([L, 0, 0, L // 2], device="cuda")
     wy, wl, wc = lab.gatedrec(x, g, None, ok, return_state=True, for_grad=True)
     for got, want in ((y, wy), (last, wl), (chunks, wc)):
         assert torch.equal(got[[0, 3]], want[[0, 3]])
-    dx, dg = torch.full((4, 70, 96), 77.0, device="cuda"), torch.full((4, 70, 96), 77.0, device="cuda")
+    dx, dg = torch.full((4, L, 96), 77.0, device="cuda"), torch.full((4, L, 96), 77.0, device="cuda")
     dh0 = torch.full((4, 96), 77.0, device="cuda")
     lab.based_gatedrec_bwd(x, g, x, chunks, dx, dg, None, dh0, n)
     assert lab.based_get_device_error() == 1
