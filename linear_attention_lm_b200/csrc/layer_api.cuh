@@ -44,11 +44,15 @@ inline long long row_ctas(int threads) {
   return (threads > kLnThreads ? 1LL : 2LL) * device_sm_count();
 }
 
+// Lanes of a row of up to 256 values at 8 per lane.
+inline int row_lanes_for(int D) { return D <= 32 ? 4 : D <= 64 ? 8 : D <= 128 ? 16 : 32; }
+
 template <typename T, int V, int E>
 based_status_t launch_layernorm_fwd(LnFwdParams p, cudaStream_t st) {
   p.row_warps = row_warps_for(p.D, E);
+  p.lanes = row_lanes_for(p.D);
   const int threads = row_threads(p.row_warps);
-  const long long want = ceil_div(p.rows, threads / (p.row_warps * 32));
+  const long long want = ceil_div(p.rows, threads / (ln_sub(E) ? p.lanes : p.row_warps * 32));
   const long long most = row_ctas(threads);
   const dim3 grid((unsigned)(want < most ? want : most));
   auto go = [&](auto kern) -> based_status_t {
@@ -61,24 +65,25 @@ based_status_t launch_layernorm_fwd(LnFwdParams p, cudaStream_t st) {
                       : go(layernorm_fwd_kernel<T, V, E, false, kN>);
   };
   using std::integral_constant;
-  if constexpr (E > 8) {
+  if constexpr (E == 32 || (E == 16 && V < 4)) {
     if (threads == 512) return pick(integral_constant<int, 512>{});
   }
-  if constexpr (E == 16) {
+  if constexpr (E == 16 && V < 4) {
     if (threads == 1024) return pick(integral_constant<int, 1024>{});
   }
   return pick(integral_constant<int, 256>{});
 }
 
 struct LnBwdPlan {
-  int E, row_warps, threads, parts;
+  int E, row_warps, tpr, threads, parts;
 };
 LnBwdPlan plan_layernorm_bwd(long long rows, int D) {
   LnBwdPlan pl;
   pl.E = D <= 256 ? 8 : 16;
   pl.row_warps = row_warps_for(D, pl.E);
+  pl.tpr = ln_sub(pl.E) ? row_lanes_for(D) : pl.row_warps * 32;
   pl.threads = row_threads(pl.row_warps);
-  const long long want = ceil_div(rows, pl.threads / (pl.row_warps * 32));
+  const long long want = ceil_div(rows, pl.threads / pl.tpr);
   const long long most = row_ctas(pl.threads);
   pl.parts = (int)(want < most ? want : most);
   return pl;
@@ -88,11 +93,12 @@ template <typename T, int V, int E>
 based_status_t launch_layernorm_bwd(LnBwdParams p, const LnBwdPlan& pl, float* dw, float* db,
                                     cudaStream_t st) {
   p.row_warps = pl.row_warps;
+  p.lanes = pl.tpr;
   if (pl.parts > 0) {
     auto go = [&](auto n, auto row_warps) {
       constexpr int kN = decltype(n)::value;
       auto kern = layernorm_bwd_kernel<T, V, E, kN, decltype(row_warps)::value>;
-      const size_t smem = LnBwdShape<T, V, E, kN>::smem(pl.row_warps * 32, p.D);
+      const size_t smem = LnBwdShape<T, V, E, kN>::smem(pl.tpr, p.D);
       return set_smem(kern, smem) &&
              launch_dependent(kern, dim3((unsigned)pl.parts), dim3(kN), smem, st, p);
     };
@@ -325,8 +331,9 @@ based_status_t based_layernorm_fwd(const void* x, const void* residual, const fl
   return for_vector(dt, D, [&](auto t, auto v) {
     using T = decltype(t);
     constexpr int V = decltype(v)::value;
-    return D <= 256 ? launch_layernorm_fwd<T, V, 8>(p, st)
-                    : launch_layernorm_fwd<T, V, (V >= 4 ? 32 : 16)>(p, st);
+    return D <= 256                 ? launch_layernorm_fwd<T, V, 8>(p, st)
+           : D <= 512 || V < 4      ? launch_layernorm_fwd<T, V, 16>(p, st)
+                                    : launch_layernorm_fwd<T, V, (V < 4 ? 16 : 32)>(p, st);
   });
 }
 

@@ -35,11 +35,17 @@ __device__ __forceinline__ void row_barrier(int warp, int row_warps) {
 }
 
 // Sums of N values over the threads of a row: row_warps warps of the CTA, this
-// one the wr-th.  `red` holds N floats per warp and is free again after the
-// row's next barrier.
-template <int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], float* red, int warp, int wr,
-                                        int row_warps) {
+// one the wr-th, or (kSub) tpr lanes of a warp, a power of two.  `red` holds N
+// floats per warp and is free again after the row's next barrier.
+template <int N, bool kSub>
+__device__ __forceinline__ void row_sum(float (&v)[N], float* red, int warp, int wr, int row_warps,
+                                        int tpr) {
+  if constexpr (kSub) {
+    for (int o = tpr / 2; o > 0; o /= 2)
+#pragma unroll
+      for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
+    return;
+  }
 #pragma unroll
   for (int n = 0; n < N; ++n) v[n] = warp_sum(v[n]);
   if (row_warps == 1) return;
@@ -63,20 +69,26 @@ struct LnFwdParams {
   void *y, *resid_out;
   float *mean, *rstd;
   long long rows;
-  int D, row_warps;
+  int D, row_warps, lanes;
   float eps;
 };
 
-// E values per thread in vectors of V; a group of row_warps warps takes every
-// (number of groups)-th row and loads the next one before it works on this one.
+// Rows of up to 256 values (E = 8) take 4 to 32 lanes of a warp, so that a warp
+// works on up to eight rows (524288 x 32 bf16 with residual: 163 us with a warp per
+// row, LNF32 here); longer ones one warp or several.
+__host__ __device__ constexpr bool ln_sub(int E) { return E == 8; }
+
+// E values per thread in vectors of V; a group of threads takes every (number of
+// groups)-th row and loads the next one before it works on this one.
 template <typename T, int V, int E, bool kResidual, int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
     layernorm_fwd_kernel(const LnFwdParams p) {
   constexpr int NV = E / V;
   __shared__ float red[2][32];
+  constexpr bool kSub = ln_sub(E);
+  const int tpr = kSub ? p.lanes : p.row_warps * 32, rpb = kThreads / tpr;
+  const int group = threadIdx.x / tpr, lane = threadIdx.x - group * tpr;  // lane: in the row
   const int warp = threadIdx.x >> 5, wr = warp % p.row_warps;
-  const int lane = threadIdx.x - (warp - wr) * 32;  // thread index in the row
-  const int tpr = p.row_warps * 32, rpb = blockDim.x / tpr;
   const float inv_d = 1.0f / p.D;
   umma::grid_dep_wait();
 
@@ -92,17 +104,20 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
       }
     }
   };
-  long long row = (long long)blockIdx.x * rpb + warp / p.row_warps;
+  long long row = (long long)blockIdx.x * rpb + group;
   const long long step = (long long)gridDim.x * rpb;
+  // the rows of a warp stay together: its first one decides
+  const int after = kSub ? group % (32 / tpr) : 0;
   if (row < p.rows) fetch(row);
-  for (; row < p.rows; row += step) {
+  for (; row - after < p.rows; row += step) {
+    const bool live = !kSub || row < p.rows;
     const size_t off = (size_t)row * p.D;
     float f[NV][V];
     float sum[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * tpr + lane) * V;
-      const bool in = c < p.D;
+      const bool in = live && c < p.D;
       if (kResidual) {
 #pragma unroll
         for (int e = 0; e < V; ++e) x[i].set(e, x[i].get(e) + r[i].get(e));
@@ -115,28 +130,28 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
       }
     }
     if (row + step < p.rows) fetch(row + step);
-    row_sum<1>(sum, red[0], warp, wr, p.row_warps);
+    row_sum<1, kSub>(sum, red[0], warp, wr, p.row_warps, tpr);
     const float mean = sum[0] * inv_d;
     float sq[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const bool in = (i * tpr + lane) * V < p.D;
+      const bool in = live && (i * tpr + lane) * V < p.D;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         f[i][e] = in ? f[i][e] - mean : 0.0f;
         sq[0] += f[i][e] * f[i][e];
       }
     }
-    row_sum<1>(sq, red[1], warp, wr, p.row_warps);
+    row_sum<1, kSub>(sq, red[1], warp, wr, p.row_warps, tpr);
     const float rstd = 1.0f / sqrtf(sq[0] * inv_d + p.eps);
-    if (lane == 0) {
+    if (live && lane == 0) {
       if (p.mean) p.mean[row] = mean;
       if (p.rstd) p.rstd[row] = rstd;
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * tpr + lane) * V;
-      if (c < p.D) {
+      if (live && c < p.D) {
         float w[V], b[V];
         load_f32<V>(p.w + c, w);
 #pragma unroll
@@ -156,7 +171,7 @@ struct LnBwdParams {
   const float *w, *mean, *rstd, *dresid;
   float *dx, *parts;
   long long rows;
-  int D, row_warps;
+  int D, row_warps, lanes;
 };
 
 // A thread owns its columns for all the rows of its group and sums dweight and
@@ -264,10 +279,11 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
   constexpr int NV = Shape::NV, kStages = Shape::kStages;
   extern __shared__ __align__(16) unsigned char ln_smem[];
   __shared__ float red[2][64];
+  constexpr bool kSub = ln_sub(E);
   const int row_warps = kRowWarps ? kRowWarps : p.row_warps;
+  const int tpr = kSub ? p.lanes : row_warps * 32, rpb = kThreads / tpr;
+  const int group = threadIdx.x / tpr, lane = threadIdx.x - group * tpr;
   const int warp = threadIdx.x >> 5, wr = warp % row_warps;
-  const int lane = threadIdx.x - (warp - wr) * 32;
-  const int tpr = row_warps * 32, rpb = kThreads / tpr;
   umma::grid_dep_wait();
 
   // this thread's E columns: vector i starts at column col(i)
@@ -279,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
   for (int j = 0; j < E / 2; ++j) dw[j] = db[j] = zero;
   load_pairs<float, V, NV>(w, [&](int i) { return p.w + col(i); }, in);
   // vector i of an array (0: x, 1: dy, 2: dresid) of this thread's row in a stage
-  const int group = warp / row_warps, row_bytes = Shape::kShare ? Shape::shared_row(p.D) : 0,
+  const int row_bytes = Shape::kShare ? Shape::shared_row(p.D) : 0,
             array_bytes = Shape::pieces(p.D * (int)sizeof(T));
   auto slot = [&](int stage, int array, int i, long long row) -> unsigned char* {
     const int size = array == 2 ? Shape::kR : Shape::kX;
@@ -327,7 +343,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
   float mean = 0.0f, rstd = 0.0f;
   if (row < p.rows) mean = p.mean[row], rstd = p.rstd[row];
   int buf = 0, stage = 0;
-  for (; row < p.rows; row += step) {
+  const int after = kSub ? group % (32 / tpr) : 0;
+  for (; row - after < p.rows; row += step) {
+    const bool live = !kSub || row < p.rows;
+    auto inside = [&](int i) { return live && in(i); };
     const size_t off = (size_t)row * p.D;
     float next_mean = 0.0f, next_rstd = 0.0f;
     if (row + step < p.rows) next_mean = p.mean[row + step], next_rstd = p.rstd[row + step];
@@ -340,8 +359,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
         else return from + off + col(i);
       };
     };
-    load_pairs<T, V, NV>(xh, input(x, 0), in);
-    load_pairs<T, V, NV>(g, input(dy, 1), in);
+    load_pairs<T, V, NV>(xh, input(x, 0), inside);
+    load_pairs<T, V, NV>(g, input(dy, 1), inside);
     // into the slot of the row before
     if constexpr (Shape::kAhead)
       fetch(row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
@@ -357,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
       db[j] = db[j] + g[j];
     }
     float s[2] = {f2_get(s0).x + f2_get(s0).y, f2_get(s1).x + f2_get(s1).y};
-    row_sum<2>(s, red[buf], warp, wr, row_warps);
+    row_sum<2, kSub>(s, red[buf], warp, wr, row_warps, tpr);
     buf ^= 1;
     const F2 c0 = f2(-s[0] * inv_d, -s[0] * inv_d), c1 = f2(-s[1] * inv_d, -s[1] * inv_d);
 #pragma unroll
@@ -370,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
             if constexpr (Shape::kAhead) return reinterpret_cast<const float*>(slot(stage, 2, i, row));
             else return p.dresid + off + col(i);
           },
-          in);
+          inside);
 #pragma unroll
       for (int j = 0; j < E / 2; ++j) g[j] = f2_fma(g[j], r2, xh[j]);
     } else {
@@ -378,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
       for (int j = 0; j < E / 2; ++j) g[j] = g[j] * r2;
     }
     float* dx = p.dx + off + lane * V;
-    store_pairs<V, NV>(g, [&](int i) { return dx + i * tpr * V; }, in);
+    store_pairs<V, NV>(g, [&](int i) { return dx + i * tpr * V; }, inside);
     mean = next_mean;
     rstd = next_rstd;
     stage = stage + 1 == kStages ? 0 : stage + 1;
