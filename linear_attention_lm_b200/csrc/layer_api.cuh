@@ -35,13 +35,16 @@ inline int row_warps_for(int D, int E) {
   return w;
 }
 
-// Threads of a CTA for rows of row_warps warps, and the CTAs that run at once: two of
-// 256 threads per SM, one of more (4000 x 8192 bf16 gradient: 70 us, 79 in two waves).
+// Threads of a CTA for rows of row_warps warps, and the CTAs that run at once: one per
+// SM of more than 256 threads (4000 x 8192 bf16 gradient: 70 us, 79 in two waves), two
+// of 256, and more where a thread has only 8 values in flight (262144 x 64 bf16,
+// forward: 31.0 us with two, 24.4 with four, 29.2 with six; gradient 38.9 with two, 35.8
+// with three).
 inline int row_threads(int row_warps) {
   return row_warps * 32 > kLnThreads ? row_warps * 32 : kLnThreads;
 }
-inline long long row_ctas(int threads) {
-  return (threads > kLnThreads ? 1LL : 2LL) * device_sm_count();
+inline long long row_ctas(int threads, int per_sm = 2) {
+  return (threads > kLnThreads ? 1LL : per_sm) * device_sm_count();
 }
 
 // Lanes of a row of up to 256 values at 8 per lane.
@@ -53,7 +56,7 @@ based_status_t launch_layernorm_fwd(LnFwdParams p, cudaStream_t st) {
   p.lanes = row_lanes_for(p.D);
   const int threads = row_threads(p.row_warps);
   const long long want = ceil_div(p.rows, threads / (ln_sub(E) ? p.lanes : p.row_warps * 32));
-  const long long most = row_ctas(threads);
+  const long long most = row_ctas(threads, E == 8 ? 4 : 2);
   const dim3 grid((unsigned)(want < most ? want : most));
   auto go = [&](auto kern) -> based_status_t {
     if (!launch_dependent(kern, grid, dim3(threads), 0, st, p)) return BASED_ERR_CUDA;
@@ -84,7 +87,7 @@ LnBwdPlan plan_layernorm_bwd(long long rows, int D) {
   pl.tpr = ln_sub(pl.E) ? row_lanes_for(D) : pl.row_warps * 32;
   pl.threads = row_threads(pl.row_warps);
   const long long want = ceil_div(rows, pl.threads / pl.tpr);
-  const long long most = row_ctas(pl.threads);
+  const long long most = row_ctas(pl.threads, pl.E == 8 ? 3 : 2);
   pl.parts = (int)(want < most ? want : most);
   return pl;
 }

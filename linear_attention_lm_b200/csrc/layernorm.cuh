@@ -75,7 +75,7 @@ struct LnFwdParams {
 
 // Rows of up to 256 values (E = 8) take 4 to 32 lanes of a warp, so that a warp
 // works on up to eight rows (524288 x 32 bf16 with residual: 163 us with a warp per
-// row, LNF32 here); longer ones one warp or several.
+// row, 25 here); longer ones one warp or several.
 __host__ __device__ constexpr bool ln_sub(int E) { return E == 8; }
 
 // E values per thread in vectors of V; a group of threads takes every (number of
