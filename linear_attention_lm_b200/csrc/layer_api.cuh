@@ -38,8 +38,8 @@ inline int row_warps_for(int D, int E) {
 // Threads of a CTA for rows of row_warps warps, and the CTAs that run at once: one per
 // SM of more than 256 threads (4000 x 8192 bf16 gradient: 70 us, 79 in two waves), two
 // of 256, and more where a thread has only 8 values in flight (262144 x 64 bf16,
-// forward: 31.0 us with two, 24.4 with four, 29.2 with six; gradient 38.9 with two, 35.8
-// with three).
+// forward: 31.0 us with two, 24.4 with four, 29.2 with six; gradient, whole
+// vectors of four, 38.9 with two, 35.8 with three).
 inline int row_threads(int row_warps) {
   return row_warps * 32 > kLnThreads ? row_warps * 32 : kLnThreads;
 }
@@ -87,7 +87,7 @@ LnBwdPlan plan_layernorm_bwd(long long rows, int D) {
   pl.tpr = ln_sub(pl.E) ? row_lanes_for(D) : pl.row_warps * 32;
   pl.threads = row_threads(pl.row_warps);
   const long long want = ceil_div(rows, pl.threads / pl.tpr);
-  const long long most = row_ctas(pl.threads, pl.E == 8 ? 3 : 2);
+  const long long most = row_ctas(pl.threads, pl.E == 8 && D % 4 == 0 ? 3 : 2);
   pl.parts = (int)(want < most ? want : most);
   return pl;
 }

@@ -81,14 +81,15 @@ __host__ __device__ constexpr bool ln_sub(int E) { return E == 8; }
 // E values per thread in vectors of V; a group of threads takes every (number of
 // groups)-th row and loads the next one before it works on this one.
 template <typename T, int V, int E, bool kResidual, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : E == 8 ? 4 : 2)
     layernorm_fwd_kernel(const LnFwdParams p) {
   constexpr int NV = E / V;
   __shared__ float red[2][32];
   constexpr bool kSub = ln_sub(E);
   const int tpr = kSub ? p.lanes : p.row_warps * 32, rpb = kThreads / tpr;
-  const int group = threadIdx.x / tpr, lane = threadIdx.x - group * tpr;  // lane: in the row
   const int warp = threadIdx.x >> 5, wr = warp % p.row_warps;
+  const int group = kSub ? threadIdx.x / tpr : warp / p.row_warps;
+  const int lane = kSub ? threadIdx.x - group * tpr : threadIdx.x - (warp - wr) * 32;  // in the row
   const float inv_d = 1.0f / p.D;
   umma::grid_dep_wait();
 
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
   // the rows of a warp stay together: its first one decides
   const int after = kSub ? group % (32 / tpr) : 0;
   if (row < p.rows) fetch(row);
-  for (; row - after < p.rows; row += step) {
+  for (; row < p.rows + after; row += step) {
     const bool live = !kSub || row < p.rows;
     const size_t off = (size_t)row * p.D;
     float f[NV][V];
@@ -273,7 +274,7 @@ __device__ __forceinline__ void store_pairs(const F2* v, At at, In in) {
 
 // kRowWarps: warps of a row; 0: p.row_warps (rows that are not whole vectors of four).
 template <typename T, int V, int E, int kThreads, int kRowWarps>
-__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : E == 8 && V == 4 ? 3 : 2)
     layernorm_bwd_kernel(const LnBwdParams p) {
   using Shape = LnBwdShape<T, V, E, kThreads>;
   constexpr int NV = Shape::NV, kStages = Shape::kStages;
@@ -282,8 +283,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
   constexpr bool kSub = ln_sub(E);
   const int row_warps = kRowWarps ? kRowWarps : p.row_warps;
   const int tpr = kSub ? p.lanes : row_warps * 32, rpb = kThreads / tpr;
-  const int group = threadIdx.x / tpr, lane = threadIdx.x - group * tpr;
   const int warp = threadIdx.x >> 5, wr = warp % row_warps;
+  const int group = kSub ? threadIdx.x / tpr : warp / row_warps;
+  const int lane = kSub ? threadIdx.x - group * tpr : threadIdx.x - (warp - wr) * 32;
   umma::grid_dep_wait();
 
   // this thread's E columns: vector i starts at column col(i)
@@ -344,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
   if (row < p.rows) mean = p.mean[row], rstd = p.rstd[row];
   int buf = 0, stage = 0;
   const int after = kSub ? group % (32 / tpr) : 0;
-  for (; row - after < p.rows; row += step) {
+  for (; row < p.rows + after; row += step) {
     const bool live = !kSub || row < p.rows;
     auto inside = [&](int i) { return live && in(i); };
     const size_t off = (size_t)row * p.D;

@@ -73,7 +73,7 @@ def ln_stats(r):
     return (np.abs(r.mean(-1)) + np.abs(r).mean(-1))[..., None]
 
 
-LN_SIZES = [(3, 1), (5, 7), (300, 64), (1, 250), (9, 256), (130, 257), (3, 999), (33, 1000),
+LN_SIZES = [(3, 1), (5, 7), (1001, 17), (77, 33), (515, 100), (21, 400), (300, 64), (1, 250), (9, 256), (130, 257), (3, 999), (33, 1000),
             (64, 1024), (700, 1024), (7, 1028), (20, 2048), (5, 4100), (3, 8191), (4, 8192),
             (2, 16383), (3, 16384)]
 
