@@ -417,6 +417,7 @@ based_status_t based_rotary_bwd(const float* dq_out, const float* dk_out, float*
  *             h_chunks are written as zero there.  An entry outside [0, L] is found
  *             by the kernel: that sequence's outputs are left untouched and
  *             BASED_ERR_INVALID_ARG is recorded (based_get_device_error).
+ * Outputs overlap neither each other nor the inputs (but h_last and h0, as said).
  * The state is fp32 throughout.  L = 0: h_last = h0.  D <= 2^20 (else
  * BASED_ERR_UNSUPPORTED).
  */

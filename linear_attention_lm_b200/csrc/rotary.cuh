@@ -71,15 +71,14 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
     c1 = c0 + (turned ? p.rot / 2 : V);
   }
   const bool two = c1 < p.D;
+  // pairs of the chunk that turn (interleaved: the rest of the last one passes)
+  const int n_turned = kInter ? min(V, p.rot / 2 - ch * V) : V;
   float cs[V], sn[V];
   if (turned) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      if (kInter && ch * V + i >= p.rot / 2) {
-        cs[i] = 1.0f;
-        sn[i] = 0.0f;
-        continue;
-      }
+      cs[i] = sn[i] = 0.0f;
+      if (i >= n_turned) continue;
       const double turns = (double)pos * p.freqs[ch * V + i];
       const float part = (float)(turns - rint(turns));
       float s, c;
@@ -95,8 +94,10 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
         Pack<T, V>& z = 2 * i < V ? a : c;
         const int e = (2 * i) % V;
         const float u = z.get(e), v = z.get(e + 1);
-        z.set(e, u * cs[i] - v * sn[i]);
-        z.set(e + 1, u * sn[i] + v * cs[i]);
+        if (i < n_turned) {
+          z.set(e, u * cs[i] - v * sn[i]);
+          z.set(e + 1, u * sn[i] + v * cs[i]);
+        }
       }
     } else {
 #pragma unroll

@@ -267,6 +267,21 @@ def test_rotary_one_of_the_two():
     assert lab.rotary(q[:, :, :0].contiguous(), None, freqs)[0].shape == (2, 4, 0, 64)
 
 
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("D,rot", [(64, 34), (64, 36), (126, 40), (51, 20)])
+def test_rotary_passes_the_rest_bit_for_bit(layout, D, rot):
+    """What is not turned is copied, infinities and NaN too, and stays out of what is."""
+    x = gen(1, (2, 3, 9, D), "bf16")
+    x[..., rot] = float("inf")
+    x[0, :, :, rot + 1:] = float("nan")
+    clean = x.clone()
+    clean[..., rot:] = 0.0
+    y = lab.rotary(x, None, lab.rotary_freqs(rot), 5, layout)[0]
+    want = lab.rotary(clean, None, lab.rotary_freqs(rot), 5, layout)[0]
+    assert torch.equal(y[..., :rot], want[..., :rot])
+    assert torch.equal(y[..., rot:].view(torch.int16), x[..., rot:].view(torch.int16))
+
+
 def test_rotary_position_out_of_range():
     """Sequences with a position outside [0, 2^31 - L] stay untouched and are reported."""
     freqs, L = lab.rotary_freqs(64), 5
