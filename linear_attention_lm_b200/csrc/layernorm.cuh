@@ -114,7 +114,9 @@ __global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : E == 8 ? 4 : 2)
     const bool live = !kSub || row < p.rows;
     const size_t off = (size_t)row * p.D;
     float f[NV][V];
-    float sum[1] = {0.0f};
+    // a thread's sum as a tree (vectors, then four parts): 5 to 11 roundings in a row
+    // instead of 32, which a mean near zero shows
+    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * tpr + lane) * V;
@@ -125,11 +127,17 @@ __global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : E == 8 ? 4 : 2)
         if (in) x[i].store(static_cast<T*>(p.resid_out) + off + c);
       }
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        f[i][e] = in ? x[i].get(e) : 0.0f;
-        sum[0] += f[i][e];
-      }
+      for (int e = 0; e < V; ++e) f[i][e] = in ? x[i].get(e) : 0.0f;
+      float t[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) t[e] = f[i][e];
+#pragma unroll
+      for (int d = V / 2; d > 0; d /= 2)
+#pragma unroll
+        for (int e = 0; e < d; ++e) t[e] += t[e + d];
+      part[i % 4] += t[0];
     }
+    float sum[1] = {(part[0] + part[1]) + (part[2] + part[3])};
     if (row + step < p.rows) fetch(row + step);
     row_sum<1, kSub>(sum, red[0], warp, wr, p.row_warps, tpr);
     const float mean = sum[0] * inv_d;
