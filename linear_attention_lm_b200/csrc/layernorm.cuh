@@ -214,17 +214,23 @@ struct LnBwdShape {
   }
 };
 
-// The row of D values at element `row * D` of an array of `rows` rows, as 16-byte
-// pieces, into `to`, by the tpr threads of a group.  Only the last row's pieces can
-// reach past the array.
-template <typename T>
+// Whether the 16-byte pieces that hold row `row` of an array of `rows` rows of n bytes
+// lie in the array: a row's last piece holds up to 15 bytes of the rows behind it, which
+// are the next one (rows of 15 bytes or more) or some more.  kShort: n may be under 15.
+template <bool kShort>
+__host__ __device__ constexpr bool pieces_inside(long long row, int n, long long rows) {
+  return row + (kShort && n < 15 ? 15 : 1) < rows;
+}
+// Row `row` of D values, as those pieces, into `to`, by the tpr threads of a group.  Of a
+// piece that may reach past the array only the row's own bytes are read.
+template <bool kShort, typename T>
 __device__ __forceinline__ void copy_row_pieces(unsigned char* to, const T* from, long long row,
                                                 int D, long long rows, int lane, int tpr) {
   const long long begin = row * D * (long long)sizeof(T);
   const int shift = (int)(begin & 15), len = shift + D * (int)sizeof(T);
   const unsigned char* src = reinterpret_cast<const unsigned char*>(from) + (begin - shift) + lane * 16;
   to += lane * 16;
-  if (row + 1 < rows) {
+  if (pieces_inside<kShort>(row, D * (int)sizeof(T), rows)) {
     for (int o = lane * 16; o < len; o += tpr * 16, src += tpr * 16, to += tpr * 16)
       umma::cp_async16(to, src, true);
   } else {
@@ -336,9 +342,10 @@ __global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : E == 8 && V == 
         }
       } else {
         unsigned char* s = ln_smem + (stage * rpb + group) * row_bytes;
-        copy_row_pieces(s, x, row, p.D, p.rows, lane, tpr);
-        copy_row_pieces(s + array_bytes, dy, row, p.D, p.rows, lane, tpr);
-        if (p.dresid) copy_row_pieces(s + 2 * array_bytes, p.dresid, row, p.D, p.rows, lane, tpr);
+        copy_row_pieces<kSub>(s, x, row, p.D, p.rows, lane, tpr);
+        copy_row_pieces<kSub>(s + array_bytes, dy, row, p.D, p.rows, lane, tpr);
+        if (p.dresid)
+          copy_row_pieces<kSub>(s + 2 * array_bytes, p.dresid, row, p.D, p.rows, lane, tpr);
       }
     }
     umma::cp_async_commit();
