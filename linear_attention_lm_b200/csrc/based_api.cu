@@ -57,6 +57,10 @@ inline based_status_t launch_status() {
   return cudaGetLastError() == cudaSuccess ? BASED_OK : BASED_ERR_CUDA;
 }
 
+// The most dynamic shared memory that launches of a kernel may ask for.  It belongs to
+// the kernel and the device, for all host threads: every launch of a kernel gives the
+// same size, the largest that any call needs.  With a call's own size, a thread with a
+// smaller call could lower it between another's setting and launch, which was refused.
 template <typename K>
 inline bool set_smem(K kernel, size_t bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -315,7 +319,7 @@ based_status_t launch_window_simt_q(const void* q, const void* k, const void* v,
                                     int BH, int L, int dh, int W, cudaStream_t st) {
   auto kern = window_simt_kernel<T, Q, SUB>;
   const size_t smem = window_simt_smem_bytes<Q>(dh);
-  if (!set_smem(kern, smem)) return BASED_ERR_CUDA;
+  if (!set_smem(kern, window_simt_smem_bytes<Q>(128))) return BASED_ERR_CUDA;
   const long long nblk = (L + Q - 1) / Q;
   if (nblk > 0x7fffffffLL || BH > 65535) return BASED_ERR_UNSUPPORTED;
   dim3 grid((unsigned)nblk, (unsigned)BH);
@@ -352,7 +356,11 @@ based_status_t launch_decode(DecodeParams p, cudaStream_t st) {
     const size_t w = (size_t)DecodeWindowLayout(p.wg, p.dh, p.W, kThreads, sizeof(T)).bytes;
     if (w > smem) smem = w;
   }
-  if (!set_smem(kern, smem)) return BASED_ERR_CUDA;
+  // the linear heads' layout, or 64 KiB of rings and the rest for four window heads of 128
+  size_t most = 65536 + (size_t)DecodeWindowLayout(4, 128, 0, kThreads, sizeof(T)).bytes;
+  if (most < sizeof(float) * DecodeLinearLayout<DV>::kSmemFloats)
+    most = sizeof(float) * DecodeLinearLayout<DV>::kSmemFloats;
+  if (!set_smem(kern, most)) return BASED_ERR_CUDA;
   const long long nblk = (long long)p.n_lin + p.n_wblk;
   p.wstride = p.n_wblk > 0 ? (int)(nblk / p.n_wblk) : 1;
   if (!launch_dependent(kern, dim3((unsigned)nblk), dim3(kThreads), smem, st, p))

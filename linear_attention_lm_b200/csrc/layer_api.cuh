@@ -101,8 +101,10 @@ based_status_t launch_layernorm_bwd(LnBwdParams p, const LnBwdPlan& pl, float* d
     auto go = [&](auto n, auto row_warps) {
       constexpr int kN = decltype(n)::value;
       auto kern = layernorm_bwd_kernel<T, V, E, kN, decltype(row_warps)::value>;
-      const size_t smem = LnBwdShape<T, V, E, kN>::smem(pl.tpr, p.D);
-      return set_smem(kern, smem) &&
+      using Shape = LnBwdShape<T, V, E, kN>;
+      const size_t smem = Shape::smem(pl.tpr, p.D);
+      static_assert(Shape::most_smem() <= 226 * 1024, "beside the static shared memory");
+      return set_smem(kern, Shape::most_smem()) &&
              launch_dependent(kern, dim3((unsigned)pl.parts), dim3(kN), smem, st, p);
     };
     constexpr std::integral_constant<int, 256> k256{};
@@ -284,6 +286,9 @@ inline GrPlan plan_gatedrec(int B, int L, int D, int group_tokens, bool padded, 
   return pl;
 }
 
+// The longest walk of the gradient, which keeps 1 KiB of shared memory per token.
+constexpr int kGrShortBwdMostL = 48;
+
 // Whether one thread per two channels walks the sequences: they are shorter than
 // a round of tiles, or so many that the walk fills the GPU.  128 x L x 1024 bf16,
 // forward, walked and in tiles: L = 16 under 10 and 26.8 us, 64: 14.6 and 26.5,
@@ -294,15 +299,15 @@ inline bool gatedrec_short(int B, int L, int D, bool forward) {
   if (L <= 16) return true;
   if (D % 2 != 0) return false;
   const long long per_sm = (long long)B * D / device_sm_count();
-  return per_sm >= 128 && L <= (forward ? (per_sm >= 800 ? 128 : 64) : 48);
+  return per_sm >= 128 && L <= (forward ? (per_sm >= 800 ? 128 : 64) : kGrShortBwdMostL);
 }
 template <typename P>
 based_status_t launch_gatedrec_short(void (*pair)(P, int), void (*single)(P, int), const P& p, int B,
-                                     size_t smem, cudaStream_t st) {
+                                     size_t smem, size_t most_smem, cudaStream_t st) {
   auto kern = p.D % 2 == 0 ? pair : single;
   const long long blocks = ceil_div((long long)B * ((p.D + 1) / 2), kGrShortThreads);
   if (blocks > 0x7fffffffLL) return BASED_ERR_UNSUPPORTED;
-  if (!set_smem(kern, smem) ||
+  if (!set_smem(kern, most_smem) ||
       !launch_dependent(kern, dim3((unsigned)blocks), dim3(kGrShortThreads), smem, st, p, B))
     return BASED_ERR_CUDA;
   return launch_status();
@@ -432,12 +437,11 @@ based_status_t based_gatedrec_fwd(const void* x, const void* g, void* y, const f
   p.x = x; p.g = g; p.y = y; p.h0 = h0; p.h_last = h_last; p.h_chunks = h_chunks;
   p.lengths = lengths; p.L = L; p.D = D;
   if (gatedrec_short(B, L, D, true)) {
-    const size_t smem = 0;
     return dt == BASED_F32
                ? launch_gatedrec_short(gatedrec_short_fwd_kernel<float, true>,
-                                       gatedrec_short_fwd_kernel<float, false>, p, B, smem, st)
+                                       gatedrec_short_fwd_kernel<float, false>, p, B, 0, 0, st)
                : launch_gatedrec_short(gatedrec_short_fwd_kernel<__nv_bfloat16, true>,
-                                       gatedrec_short_fwd_kernel<__nv_bfloat16, false>, p, B, smem,
+                                       gatedrec_short_fwd_kernel<__nv_bfloat16, false>, p, B, 0, 0,
                                        st);
   }
   return for_copies(dt, D, [&](auto t, auto cw) -> based_status_t {
@@ -473,13 +477,14 @@ based_status_t based_gatedrec_bwd(const void* x, const void* g, const void* dy,
   p.x = x; p.g = g; p.dy = dy; p.h_chunks = h_chunks; p.dh_last = dh_last;
   p.dx = dx; p.dg = dg; p.dh0 = dh0; p.lengths = lengths; p.L = L; p.D = D;
   if (gatedrec_short(B, L, D, false)) {
-    const size_t smem = sizeof(F2) * kGrShortThreads * (size_t)L;
+    const size_t token = sizeof(F2) * kGrShortThreads, smem = token * L,
+                 most = token * kGrShortBwdMostL;
     return dt == BASED_F32
                ? launch_gatedrec_short(gatedrec_short_bwd_kernel<float, true>,
-                                       gatedrec_short_bwd_kernel<float, false>, p, B, smem, st)
+                                       gatedrec_short_bwd_kernel<float, false>, p, B, smem, most, st)
                : launch_gatedrec_short(gatedrec_short_bwd_kernel<__nv_bfloat16, true>,
                                        gatedrec_short_bwd_kernel<__nv_bfloat16, false>, p, B, smem,
-                                       st);
+                                       most, st);
   }
   return for_copies(dt, D, [&](auto t, auto cw) -> based_status_t {
     using T = decltype(t);

@@ -205,12 +205,19 @@ struct LnBwdShape {
   __host__ __device__ static constexpr int shared_row(int D) {
     return 2 * pieces(D * (int)sizeof(T)) + pieces(D * 4);
   }
-  static size_t smem(int tpr, int D) {
+  static constexpr size_t smem(int tpr, int D) {
     const size_t ring = kOwn     ? (size_t)kStages * kThread * kThreads
                         : kShare ? (size_t)kStages * shared_row(D) * (kThreads / tpr)
                                  : 0;
     const size_t join = tpr < kThreads ? (size_t)D * 8 * (kThreads / tpr) : 0;
     return join > ring ? join : ring;
+  }
+  // that of the widest rows (a thread has E values) of any number of threads
+  static constexpr size_t most_smem() {
+    size_t most = 0;
+    for (int tpr = ln_sub(E) ? 4 : 32; tpr <= kThreads; tpr *= 2)
+      if (smem(tpr, tpr * E) > most) most = smem(tpr, tpr * E);
+    return most;
   }
 };
 
