@@ -57,14 +57,22 @@ inline based_status_t launch_status() {
   return cudaGetLastError() == cudaSuccess ? BASED_OK : BASED_ERR_CUDA;
 }
 
+// Whether a runtime call succeeded.  Its error does not stay behind for launch_status()
+// of the next call.
+inline bool succeeded(cudaError_t e) {
+  if (e == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
+}
+
 // The most dynamic shared memory that launches of a kernel may ask for.  It belongs to
 // the kernel and the device, for all host threads: every launch of a kernel gives the
 // same size, the largest that any call needs.  With a call's own size, a thread with a
 // smaller call could lower it between another's setting and launch, which was refused.
 template <typename K>
 inline bool set_smem(K kernel, size_t bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)bytes) == cudaSuccess;
+  return succeeded(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        (int)bytes));
 }
 
 // Launch as a programmatic dependent of the previous kernel in the stream: the
@@ -90,7 +98,7 @@ bool launch_dependent(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...) == cudaSuccess;
+  return succeeded(cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...));
 }
 
 // Shared argument checks of the prefill entry points.  Null tensor pointers
@@ -140,8 +148,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult qr;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &qr) !=
-            cudaSuccess ||
+    if (!succeeded(cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &qr)) ||
         qr != cudaDriverEntryPointSuccess)
       p = nullptr;
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
@@ -184,8 +191,8 @@ bool make_head_out_map(CUtensorMap* m, void* y, int D, int L, int BH) {
 
 int device_sm_count() {
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+  if (!succeeded(cudaGetDevice(&dev))) return 148;
+  if (!succeeded(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) || n <= 0)
     return 148;
   return n;
 }
@@ -409,12 +416,12 @@ based_status_t launch_proj(const void* x, const void* w, ProjParams p, cudaStrea
   cfg.numAttrs = 1;  // the occupancy query below takes the cluster shape only
   cfg.gridDim = dim3(2 * (unsigned)((device_sm_count() + 1) / 2), 1, 1);
   int max_clusters = 0;
-  if (cudaOccupancyMaxActiveClusters(&max_clusters, kern, &cfg) != cudaSuccess || max_clusters <= 0)
+  if (!succeeded(cudaOccupancyMaxActiveClusters(&max_clusters, kern, &cfg)) || max_clusters <= 0)
     return BASED_ERR_CUDA;
   const long long pairs = tiles < max_clusters ? tiles : max_clusters;
   cfg.gridDim = dim3(2 * (unsigned)pairs, 1, 1);
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, kern, xm, wm, hm, ym, p) != cudaSuccess) return BASED_ERR_CUDA;
+  if (!succeeded(cudaLaunchKernelEx(&cfg, kern, xm, wm, hm, ym, p))) return BASED_ERR_CUDA;
   return launch_status();
 }
 
@@ -549,7 +556,7 @@ namespace {
 // Device address of g_noalloc_scratch on the current device.
 based_status_t noalloc_scratch(float** addr) {
   void* p = nullptr;
-  if (cudaGetSymbolAddress(&p, g_noalloc_scratch) != cudaSuccess || p == nullptr)
+  if (!succeeded(cudaGetSymbolAddress(&p, g_noalloc_scratch)) || p == nullptr)
     return BASED_ERR_CUDA;
   *addr = static_cast<float*>(p);
   return BASED_OK;
@@ -563,7 +570,7 @@ int based_abi_version(void) { return 1; }
 
 int based_binary_version(void) {
   cudaFuncAttributes a;
-  if (cudaFuncGetAttributes(&a, linattn_tc_kernel<64, false>) != cudaSuccess) return -1;
+  if (!succeeded(cudaFuncGetAttributes(&a, linattn_tc_kernel<64, false>))) return -1;
   return a.binaryVersion;
 }
 
@@ -890,22 +897,22 @@ based_status_t based_debug_stall(int which, long long wait_limit_ns) {
     return BASED_ERR_INVALID_ARG;
   if (wait_limit_ns <= 0) return BASED_ERR_INVALID_ARG;
   const uint64_t limit = static_cast<uint64_t>(wait_limit_ns);
-  if (cudaDeviceSynchronize() != cudaSuccess) return BASED_ERR_CUDA;
-  if (cudaMemcpyToSymbol(g_stall_test, &which, sizeof(int)) != cudaSuccess ||
-      cudaMemcpyToSymbol(umma::g_wait_limit_ns, &limit, sizeof(uint64_t)) != cudaSuccess)
+  if (!succeeded(cudaDeviceSynchronize())) return BASED_ERR_CUDA;
+  if (!succeeded(cudaMemcpyToSymbol(g_stall_test, &which, sizeof(int))) ||
+      !succeeded(cudaMemcpyToSymbol(umma::g_wait_limit_ns, &limit, sizeof(uint64_t))))
     return BASED_ERR_CUDA;
   return BASED_OK;
 }
 
 based_status_t based_get_device_error(based_stream_t stream) {
-  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
+  if (!succeeded(cudaStreamSynchronize(static_cast<cudaStream_t>(stream))))
     return BASED_ERR_CUDA;
   int v = BASED_OK;
-  if (cudaMemcpyFromSymbol(&v, g_device_status, sizeof(int)) != cudaSuccess)
+  if (!succeeded(cudaMemcpyFromSymbol(&v, g_device_status, sizeof(int))))
     return BASED_ERR_CUDA;
   if (v != BASED_OK) {
     const int ok = BASED_OK;
-    if (cudaMemcpyToSymbol(g_device_status, &ok, sizeof(int)) != cudaSuccess)
+    if (!succeeded(cudaMemcpyToSymbol(g_device_status, &ok, sizeof(int))))
       return BASED_ERR_CUDA;
   }
   return static_cast<based_status_t>(v);

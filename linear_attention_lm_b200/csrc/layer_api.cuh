@@ -253,7 +253,7 @@ bool launch_gatedrec(void (*kern)(P), const P& p, long long clusters, size_t sme
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = p.N > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess;
+  return succeeded(cudaLaunchKernelEx(&cfg, kern, p));
 }
 
 // The cut of a recurrence: G groups of lanes per warp (64 / G channels per CTA) and N

@@ -1,4 +1,5 @@
-"""Host side of the launches: calls from two host threads at once."""
+"""Host side of the launches: calls from two host threads at once, and a call after one
+whose launch was refused."""
 import ctypes
 import os
 import subprocess
@@ -127,3 +128,28 @@ def test_two_host_threads(hammer, make, sizes):
     for (_, _, _, outs), w in zip(made, want):
         assert all(torch.equal(a, b) for a, b in zip(outs, w))
     assert lab.based_get_device_error() == 0
+
+
+def test_a_refused_launch_leaves_the_next_call_alone():
+    """A launch on the legacy stream is refused by the runtime while another stream, which
+    that one waits for, is being captured; the calls after it say nothing of it."""
+    rt = ctypes.CDLL("libcudart.so.12")
+    x, g, h = (normal(i, 4, 64) for i in range(3))
+    y = torch.empty_like(x)
+    held = h.clone()
+    stream, graph = ctypes.c_void_p(), ctypes.c_void_p()
+    torch.cuda.synchronize()
+    assert rt.cudaStreamCreate(ctypes.byref(stream)) == 0
+    assert rt.cudaStreamBeginCapture(stream, 1) == 0
+    try:
+        with pytest.raises(lab.BasedError) as e:
+            lab.based_gatedrec_step(x, g, h, y, stream=0)
+    finally:
+        rt.cudaStreamEndCapture(stream, ctypes.byref(graph))
+        rt.cudaStreamDestroy(stream)
+        rt.cudaGetLastError()
+    assert e.value.status == 3
+    lab.based_gatedrec_step(x, g, h, y)
+    torch.cuda.synchronize()
+    want = held * torch.sigmoid(g) + x * torch.sigmoid(-g)
+    assert torch.allclose(h, want, rtol=1e-5, atol=1e-5)
