@@ -518,23 +518,27 @@ __global__ void __launch_bounds__(kGrThreads, 2) gatedrec_bwd_kernel(const GrBwd
         xv[s] = f2_fma(xv[s], minus, h);  // h_{t-1} - x_t
         h = f2_fma(a[s], h, u);
       }
-        float *dx = p.dx + seq + (size_t)first(k) * p.D, *dg = p.dg + seq + (size_t)first(k) * p.D;
+      float *dx = p.dx + seq + (size_t)first(k) * p.D, *dg = p.dg + seq + (size_t)first(k) * p.D;
       uint32_t at = (uint32_t)((w * G + grp) * S + S - 1) * p.D + c;
-      auto step = [&](int s, bool in) {
-        const F2 lt = e + d[s];
-        const F2 dxv = n[s] * lt;  // past the end n is 0
-        e = a[s] * lt;
-        if (in) {
+      if (t0 + S <= end) {
+#pragma unroll
+        for (int s = S - 1; s >= 0; --s, at -= p.D) {
+          const F2 lt = e + d[s], dxv = n[s] * lt;
+          e = a[s] * lt;
           gr_store<kPair>(dx + at, dxv, two);
           gr_store<kPair>(dg + at, dxv * xv[s] * a[s], two);
         }
-      };
-      if (t0 + S <= p.L) {
-#pragma unroll
-        for (int s = S - 1; s >= 0; --s, at -= p.D) step(s, true);
       } else {
 #pragma unroll
-        for (int s = S - 1; s >= 0; --s, at -= p.D) step(s, t0 + s < p.L);
+        for (int s = S - 1; s >= 0; --s, at -= p.D) {
+          const bool token = t0 + s < end;
+          const F2 lt = e + d[s], dxv = n[s] * lt;
+          e = a[s] * lt;  // past the end a is 1
+          if (t0 + s < p.L) {  // zero past the end, whatever dh_last is
+            gr_store<kPair>(dx + at, token ? dxv : zero, two);
+            gr_store<kPair>(dg + at, token ? dxv * xv[s] * a[s] : zero, two);
+          }
+        }
       }
     }
   }
