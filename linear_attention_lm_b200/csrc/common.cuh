@@ -57,7 +57,8 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
 
 // 2^x by the hardware approximation (PTX ex2.approx.ftz.f32: one special-function
 // instruction, relative error about 2^-22, subnormal results flushed to zero).
-// Used for softmax weights, which are rounded to bf16 right after.
+// Used for softmax weights, which are rounded to bf16 right after, and for the gated
+// recurrence's gates, which state their error.
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

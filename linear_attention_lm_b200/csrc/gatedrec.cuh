@@ -15,10 +15,16 @@ namespace based {
 
 constexpr int kGrChunk = 64;  // tokens between two saved states
 
-// a = sigmoid(g) and n = 1 - a.  The smaller of the two is formed with its full
-// relative precision, t = e / (1 + e) with e = exp(-|g|), and the other is its
-// complement to 1, so that a slow decay (1 - a << 1) keeps its rate.  The
-// reciprocal is the hardware's (about 2^-23 off; its argument is in [1, 2]).
+// a = sigmoid(g) and n = 1 - a.  The smaller of the two is t = e / (1 + e) with
+// e = exp(-|g|), the other is its complement to 1.  t is off by about 2^-21 + |g| 2^-23
+// of itself: the hardware's 2^x and reciprocal (2^-22 and 2^-23), the rounding of the
+// exponent, which grows with |g|, and that of the product; beyond |g| = 87 it is 0.
+//
+// Just below 1 fp32 has steps of 2^-24, so a alone would hold a slow decay's rate n only
+// to 2^-25 (0.07% at a logit of 10, up to half at 16), the same way at every token of a
+// constant gate.  What decays a state takes the rate from n instead: the map of a lane's
+// tokens by map_kept, the walk token by token by gate_rest.  What stays is the rounding
+// of the fp32 state itself, at each update.
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -30,7 +36,7 @@ struct Gate {
 __device__ __forceinline__ Gate gate_of(float g) {
   const float e = ex2_approx(-1.4426950408889634f * fabsf(g));
   const float t = e * rcp_approx(1.0f + e);
-  const float u = 1.0f - t;
+  const float u = __fsub_rn(1.0f, t);  // of the rounded t, not contracted with its product
   return g >= 0.0f ? Gate{u, t} : Gate{t, u};
 }
 struct Gate2 {
@@ -46,6 +52,15 @@ __device__ __forceinline__ Gate2 gate_of(F2 g2) {
   const float2 t = f2_get(t2), u = f2_get(f2_fma(t2, f2(-1.0f, -1.0f), one));
   const bool px = g.x >= 0.0f, py = g.y >= 0.0f;
   return Gate2{f2(px ? u.x : t.x, py ? u.y : t.y), f2(px ? t.x : u.x, py ? t.y : u.y)};
+}
+// What the rounded a leaves out: 1 - n = a + gate_rest, exactly (0 where a is the smaller
+// of the two).
+__device__ __forceinline__ float gate_rest(const Gate& g) {
+  return __fsub_rn(__fsub_rn(1.0f, g.a), g.n);
+}
+__device__ __forceinline__ F2 gate_rest(const Gate2& g) {
+  const F2 one = f2(1.0f, 1.0f), minus = f2(-1.0f, -1.0f);
+  return f2_fma(g.n, minus, f2_fma(g.a, minus, one));
 }
 
 // How the sequence is cut: a lane takes S tokens of two channels; a warp G groups of
@@ -118,6 +133,17 @@ __device__ __forceinline__ GrMap map_scan_groups(GrMap& m, int o, int lane) {
   return before;
 }
 __device__ __forceinline__ void map_apply(F2& h, const GrMap& m) { h = f2_fma(m.A, h, m.H); }
+// What a product of gates leaves out of 1, with one more gate 1 - n.
+__device__ __forceinline__ F2 map_lost(F2 lost, F2 n) {
+  return f2_fma(n, f2_fma(lost, f2(-1.0f, -1.0f), f2(1.0f, 1.0f)), lost);
+}
+// The product A of a lane's gates, from what it leaves out where that is under a half:
+// one rounding for all the lane's tokens, not one for each (8 x 2048 x 1024 bf16: 24.2
+// us, 24.1 without; 25.3 with what is left out summed from n times A).
+__device__ __forceinline__ F2 map_kept(F2 A, F2 lost) {
+  const float2 p = f2_get(A), l = f2_get(lost);
+  return f2(l.x < 0.5f ? 1.0f - l.x : p.x, l.y < 0.5f ? 1.0f - l.y : p.y);
+}
 
 // Maps of a CTA's warps and of a cluster's CTAs, two sets in turn.  The CTAs send
 // each other their maps with stores that complete on the receiver's barrier of
@@ -344,11 +370,13 @@ __global__ void __launch_bounds__(kGrThreads, 2) gatedrec_fwd_kernel(const GrFwd
     const T* gs = xs + S * 64;
     F2 a[S], u[S];  // h -> a h + u
     GrMap m = map_one();
+    F2 lost = f2(0.0f, 0.0f);  // 1 less the product of the gates
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       const Gate2 gt = gate_of(load_pair(gs + s * 64));
       a[s] = gt.a;
       u[s] = gt.n * load_pair(xs + s * 64);
+      lost = map_lost(lost, gt.n);
     }
     if (t0 + S > end) {  // past the end: the identity
 #pragma unroll
@@ -357,9 +385,11 @@ __global__ void __launch_bounds__(kGrThreads, 2) gatedrec_fwd_kernel(const GrFwd
           a[s] = f2(1.0f, 1.0f);
           u[s] = f2(0.0f, 0.0f);
         }
+      lost = f2(1.0f, 1.0f);  // the product
     }
 #pragma unroll
     for (int s = 0; s < S; ++s) map_then(m, GrMap{a[s], u[s]});
+    m.A = map_kept(m.A, lost);
     F2 e;
     ok = gr_round<G, false>(sh, k, w, rank, grp, p.N, lane, m, h, e, ok, [](int r) { return r; });
     if (live) {
@@ -495,9 +525,13 @@ __global__ void __launch_bounds__(kGrThreads, 2) gatedrec_bwd_kernel(const GrBwd
         }
     }
     GrMap f = map_one(), q;
+    F2 lost = zero;  // 1 less the product of the gates
 #pragma unroll
-    for (int s = 0; s < S; ++s) map_then(f, GrMap{a[s], n[s] * xv[s]});
-    q.A = f.A;
+    for (int s = 0; s < S; ++s) {
+      lost = f2_fma(n[s], f.A, lost);
+      map_then(f, GrMap{a[s], n[s] * xv[s]});
+    }
+    q.A = f.A = map_kept(f.A, lost);
     q.H = zero;
 #pragma unroll
     for (int s = S - 1; s >= 0; --s) q.H = a[s] * (q.H + d[s]);
@@ -625,18 +659,19 @@ __global__ void __launch_bounds__(kGrShortThreads) gatedrec_short_fwd_kernel(con
       gr_store<kPair>(chunk, t0 < k.len ? h : zero, k.two);
       chunk += p.D;
     }
-    F2 a[kGrBatch], u[kGrBatch];
+    F2 a[kGrBatch], r[kGrBatch], u[kGrBatch];
 #pragma unroll
     for (int s = 0; s < kGrBatch; ++s) {
       const Gate2 gt = gate_of(to_pair(g[s]));
       a[s] = gt.a;
+      r[s] = gate_rest(gt);
       u[s] = gt.n * to_pair(x[s]);
     }
     fetch(t0 + kGrBatch);
 #pragma unroll
     for (int s = 0; s < kGrBatch; ++s)
       if (t0 + s < p.L) {
-        if (t0 + s < k.len) h = f2_fma(a[s], h, u[s]);
+        if (t0 + s < k.len) h = f2_fma(a[s], h, f2_fma(r[s], h, u[s]));
         gr_store<kPair>(y + (size_t)(t0 + s) * p.D, t0 + s < k.len ? h : zero, k.two);
       }
   }
@@ -666,11 +701,12 @@ __global__ void __launch_bounds__(kGrShortThreads) gatedrec_short_bwd_kernel(con
   };
   fetch(0);
   for (int t0 = 0; t0 < k.len; t0 += kGrBatch) {
-    F2 a[kGrBatch], u[kGrBatch];
+    F2 a[kGrBatch], r[kGrBatch], u[kGrBatch];
 #pragma unroll
     for (int s = 0; s < kGrBatch; ++s) {
       const Gate2 gt = gate_of(to_pair(g[s]));
       a[s] = gt.a;
+      r[s] = gate_rest(gt);
       u[s] = gt.n * to_pair(x[s]);
     }
     fetch(t0 + kGrBatch);
@@ -678,7 +714,7 @@ __global__ void __launch_bounds__(kGrShortThreads) gatedrec_short_bwd_kernel(con
     for (int s = 0; s < kGrBatch; ++s)
       if (t0 + s < k.len) {
         before[(t0 + s) * kGrShortThreads] = h;
-        h = f2_fma(a[s], h, u[s]);
+        h = f2_fma(a[s], h, f2_fma(r[s], h, u[s]));
       }
   }
   F2 l = p.dh_last ? gr_load<kPair>(p.dh_last + state, k.two) : zero;
@@ -714,7 +750,7 @@ __global__ void __launch_bounds__(kGrShortThreads) gatedrec_short_bwd_kernel(con
       if (t1 - 1 - s >= 0) {
         const size_t at = (size_t)(t1 - 1 - s) * p.D;
         const F2 lt = l + dv[s], dxv = n[s] * lt;
-        l = a[s] * lt;
+        l = f2_fma(a[s], lt, gate_rest(Gate2{a[s], n[s]}) * lt);
         gr_store<kPair>(dx + at, dxv, k.two);
         gr_store<kPair>(dg + at, dxv * diff[s] * a[s], k.two);
       }
@@ -739,7 +775,7 @@ __global__ void __launch_bounds__(128) gatedrec_step_kernel(const T* __restrict_
 #pragma unroll
   for (int e = 0; e < V; ++e) {
     const Gate gt = gate_of(gv.get(e));
-    hv[e] = gt.a * hv[e] + gt.n * xv.get(e);
+    hv[e] = fmaf(gt.a, hv[e], fmaf(gate_rest(gt), hv[e], gt.n * xv.get(e)));
     xv.set(e, hv[e]);
   }
   store_f32<V>(h + i, hv);

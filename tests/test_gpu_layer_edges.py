@@ -54,3 +54,95 @@ def test_gatedrec_gradient_padding_is_zero_beside_a_bad_final_gradient(B, L, D, 
     for a, b in zip((dx, dg, dh0), want):
         assert torch.equal(a[..., clean], b[..., clean])
     assert lab.based_get_device_error() == 0
+
+
+# ------------------------------------------------------------------ slow decays
+
+def slow_gates(D, dtype):
+    """Logits of 11 to 17.  In fp32 the first half lies where 1 - a is halfway between two
+    multiples of 2^-24, the spacing of fp32 below 1: a rounded a is worst there."""
+    k = np.arange(D // 2)
+    n = (k % 90 + 1.5) * 2.0 ** -24
+    g = np.concatenate([np.log1p(-n) - np.log(n), np.linspace(11.0, 17.0, D - D // 2)])
+    return torch.from_numpy(g.astype(np.float32)).to(DT[dtype])
+
+
+def rates(g):
+    """1 - a in fp64, and the kernels' relative error of it: 2^x to 2^-22, its argument's
+    rounding |g| 2^-23, a division to 2^-22."""
+    g = g.double().cpu().numpy()
+    return np.exp(-g) / (1 + np.exp(-g)), 2.0 ** -20 + np.abs(g) * 2.0 ** -22
+
+
+SLOW = [(1, 16384, 64), (8, 4096, 1024), (2, 5000, 33), (1, 9000, 333), (60, 512, 1024)]
+
+
+@pytest.mark.parametrize("B,L,D", SLOW)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gatedrec_slow_decay_keeps_its_rate(B, L, D, dtype):
+    """From a state of 1, with x = 0 the state decays to (1 - n)^L, with x = 1 it stays 1;
+    and a final gradient of 1 decays to (1 - n)^L.
+
+    The state stays in (1/2, 1], where an fp32 rounding is at most 2^-25.  A lane of S
+    tokens (32 bytes of x forward, 16 backward) rounds its product of gates once, joins
+    maps once and rounds the state once for each warp or lane group: 2^-25 twice per S
+    tokens.  What a product leaves out is summed to S 2^-24 of itself, and the tokens of
+    the last lane are walked with a rounding of a and of the state each."""
+    size = 2 if dtype == "bf16" else 4
+    gates = slow_gates(D, dtype)
+    n, tau = rates(gates)
+    g = gates.cuda().expand(B, L, D).contiguous()
+    zero, one = torch.zeros(B, L, D, dtype=DT[dtype], device="cuda"), torch.ones(B, D, device="cuda")
+    want = np.exp(L * np.log1p(-n))
+
+    def bound(S, rate_error=True):
+        steps = L * 2.0 ** -24 / S + L * n * S * 2.0 ** -24 + 2 * S * 2.0 ** -24
+        return steps + (L * n * tau if rate_error else 0.0)
+
+    _, last, chunks = lab.gatedrec(zero, g, one, return_state=True, for_grad=True)
+    off = np.abs(last.double().cpu().numpy() - want) - bound(32 // size)
+    assert off.max() <= 0, off.max()
+    _, last = lab.gatedrec(torch.ones_like(zero), g, one, return_state=True)
+    off = np.abs(last.double().cpu().numpy() - 1.0) - bound(32 // size, False)
+    assert off.max() <= 0, off.max()
+    _, _, dh0 = lab.gatedrec_grad(zero, g, zero, chunks, one)
+    off = np.abs(dh0.double().cpu().numpy() - want) - bound(16 // size)
+    assert off.max() <= 0, off.max()
+
+
+@pytest.mark.parametrize("B,L,D", [(128, 48, 1024), (3, 16, 333), (4, 15, 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gatedrec_slow_decay_keeps_its_rate_in_short_sequences(B, L, D, dtype):
+    """The same where a thread walks the tokens: one rounding of the state per token, of at
+    most 2^-25 as it lies in (1/2, 1], and what is added to it first is rounded to 2^-24
+    of n."""
+    gates = slow_gates(D, dtype)
+    n, tau = rates(gates)
+    g = gates.cuda().expand(B, L, D).contiguous()
+    zero = torch.zeros(B, L, D, dtype=DT[dtype], device="cuda")
+    start = 0.6 + 0.39 * torch.rand(B, D, generator=torch.Generator("cuda").manual_seed(1), device="cuda")
+    bound = L * (2.0 ** -25 + n * (tau + 2.0 ** -23))
+    want = start.double().cpu().numpy() * np.exp(L * np.log1p(-n))
+    _, last, chunks = lab.gatedrec(zero, g, start, return_state=True, for_grad=True)
+    off = np.abs(last.double().cpu().numpy() - want) - bound
+    assert off.max() <= 0, off.max()
+    _, _, dh0 = lab.gatedrec_grad(zero, g, zero, chunks, start)
+    off = np.abs(dh0.double().cpu().numpy() - want) - bound
+    assert off.max() <= 0, off.max()
+
+
+@pytest.mark.parametrize("B,D", [(64, 1024), (5, 33)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gatedrec_step_rounds_once(B, D, dtype):
+    """The new state is the exact one, rounded once: half a step of fp32 at its size, and
+    n (|h| + |x|) times the gate's error and the roundings of n x and of what is added."""
+    gates = slow_gates(D, dtype)
+    n, tau = rates(gates)
+    h = 1 + torch.rand(B, D, generator=torch.Generator("cuda").manual_seed(2), device="cuda")
+    x, g = normal(3, (B, D), dtype), gates.cuda().expand(B, D).contiguous()
+    h64, x64 = h.double().cpu().numpy(), x.double().cpu().numpy()
+    lab.gatedrec_step(x, g, h)
+    want = h64 + n * (x64 - h64)
+    bound = np.spacing(np.float32(want) * np.float32(1 + 2.0 ** -20)) / 2 + n * (np.abs(h64) + np.abs(x64)) * (tau + 2.0 ** -22)
+    off = np.abs(h.double().cpu().numpy() - want) - bound
+    assert off.max() <= 0, off.max()
