@@ -405,7 +405,12 @@ based_status_t based_rotary_bwd(const float* dq_out, const float* dk_out, float*
  * (the "based/train" README explores a decay without giving a formula):
  *   a_t = sigmoid(g_t),  h_t = a_t h_{t-1} + (1 - a_t) x_t,  y_t = h_t
  * The gate is given as its logit: bf16 has no value between 0.996 and 1.  A
- * logit of -inf starts anew from x_t, +inf keeps the state.
+ * logit of -inf starts anew from x_t, +inf keeps the state.  Logits aside, values
+ * are finite: from a token on whose x, or whose state before it, is infinite or
+ * NaN, or whose logit is NaN, that channel of that sequence is undefined, after a
+ * logit of -inf too (products of gates may reach zero, and zero times such a state
+ * is NaN).  What lies before the token, other channels and sequences, and the
+ * zeros of the padding are as without it.
  *   x, g, y   [B, L, D] dt (y written)
  *   h0        [B, D] fp32 or NULL (zero): the state before the first token
  *   h_last    [B, D] fp32 or NULL: the state after the last token (written; may
@@ -433,6 +438,8 @@ based_status_t based_gatedrec_fwd(const void* x, const void* g, void* y, const f
  *   dh_last  [B, D] fp32 or NULL (zero);  dh0 [B, D] fp32 or NULL (written; may be dh_last)
  *   dx, dg   [B, L, D] fp32 (written; zero past a sequence's length)
  *   lengths  as in the forward
+ * A value that is not finite (logits of +-inf aside) leaves dx, dg and dh0 of its
+ * channel of its sequence undefined, and nothing else.
  */
 based_status_t based_gatedrec_bwd(const void* x, const void* g, const void* dy,
                                   const float* h_chunks, const float* dh_last, float* dx, float* dg,

@@ -146,3 +146,37 @@ def test_gatedrec_step_rounds_once(B, D, dtype):
     bound = np.spacing(np.float32(want) * np.float32(1 + 2.0 ** -20)) / 2 + n * (np.abs(h64) + np.abs(x64)) * (tau + 2.0 ** -22)
     off = np.abs(h.double().cpu().numpy() - want) - bound
     assert off.max() <= 0, off.max()
+
+
+# ------------------------------------------------------------------ values that are not finite
+
+@pytest.mark.parametrize("B,L,D", REC_SHAPES)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gatedrec_bad_values_stay_in_their_channel(B, L, D, dtype):
+    """An infinite or NaN x, a NaN logit and an infinite first state: other channels and
+    sequences, the tokens before, and the padding keep their bits."""
+    x, g, dy = (normal(i, (B, L, D), dtype) for i in range(3))
+    h0, n = normal(4, (B, D)), spread_lengths(B, L)
+    y, last, chunks = lab.gatedrec(x, g, h0, n, return_state=True, for_grad=True)
+    grads = lab.gatedrec_grad(x, g, dy, chunks, None, n)
+    t = int(n[1]) // 2  # inside the first two sequences
+    x2, g2, h2 = x.clone(), g.clone(), h0.clone()
+    x2[0, t, 0::5], g2[1, t, 2::5], h2[1, 4::5] = float("inf"), float("nan"), float("inf")
+    x2[1, t, 0::5] = float("nan")
+    y2, last2, chunks2 = lab.gatedrec(x2, g2, h2, n, return_state=True, for_grad=True)
+    more = lab.gatedrec_grad(x2, g2, dy, chunks2, None, n)
+    past = torch.arange(L, device="cuda")[None, :] >= n[:, None]
+    bad = torch.zeros(B, 1, D, dtype=torch.bool, device="cuda")
+    bad[:2, :, 0::5] = bad[1, :, 2::5] = bad[1, :, 4::5] = True
+    before = torch.arange(L, device="cuda")[None, :, None] < t
+    before = before.expand(B, L, D).clone()
+    before[1, :, 4::5] = False  # a bad first state
+    same = ~bad | before | past[..., None]
+    assert torch.equal(y2[same], y[same])
+    assert torch.equal(last2[~bad[:, 0]], last[~bad[:, 0]])
+    assert torch.equal(chunks2[~bad.expand_as(chunks)], chunks[~bad.expand_as(chunks)])
+    for a, b in zip(more[:2], grads[:2]):
+        assert torch.equal(a[(~bad | past[..., None])], b[(~bad | past[..., None])])
+    assert torch.equal(more[2][~bad[:, 0]], grads[2][~bad[:, 0]])
+    assert not y2[past].any() and not more[0][past].any() and not more[1][past].any()
+    assert lab.based_get_device_error() == 0
