@@ -180,3 +180,16 @@ def test_gatedrec_bad_values_stay_in_their_channel(B, L, D, dtype):
     assert torch.equal(more[2][~bad[:, 0]], grads[2][~bad[:, 0]])
     assert not y2[past].any() and not more[0][past].any() and not more[1][past].any()
     assert lab.based_get_device_error() == 0
+
+
+def test_layernorm_largest_values():
+    """|r| of 7e16 at the widest rows: the squares' sum stays below fp32's largest.  A row
+    of ones and minus ones scaled by it gives the row's own norm, up to the roundings of
+    two sums of at most 80 steps (as in the parity test) on either side."""
+    for D in (64, 999, 16384):
+        x = torch.ones(3, D, device="cuda")
+        x[:, ::2] = -1.0
+        w, b = torch.ones(D, device="cuda"), torch.zeros(D, device="cuda")
+        want = lab.layernorm(x, w, b, eps=1e-12)
+        got = lab.layernorm(x * 7e16, w, b, eps=1e-12)
+        assert float((got - want).abs().max()) <= 4 * 80 * 2.0 ** -24
