@@ -74,14 +74,16 @@ __device__ __forceinline__ F2 gate_rest(const Gate2& g) {
 // copies its own tokens of the next tiles into a ring of kGrStages slots
 // (cp.async), so loads run ahead of the barriers and hold no registers.
 //
-// What bounds it: about 24 instructions per value forward and 50 in the gradient
-// (the gate alone has two special-function and ten other instructions) keep the SMs
-// half busy, and the barriers of a round cost the rest; at 86% of the SMs (256
-// CTAs of 296) 8 x 2048 x 1024 bf16, 101 MB, takes 23.8 us (4.2 TB/s; a copy of as
-// many bytes 19 us) and its gradient, 235 MB, 46 us (5.1 TB/s).  One thread per
-// channel took 1221 and (padded batch) 2194 us; loads into registers one tile
-// ahead 39.0 and 64.8 us.  1 x 16384 x 1024 (N = 8): 30.6 us, of which the
-// exchanges between CTAs, about 0.9 us per round, are 7.
+// What bounds it: the latency of a round.  About 26 instructions per value forward and
+// 46 in the gradient (the gate alone has two special-function and ten other
+// instructions) fill 56 and 50% of the issue slots, with 13 warps per SM between the
+// barriers of a round, on 86% of the SMs (256 CTAs of 296).  8 x 2048 x 1024 bf16, 101
+// MB: 24.2 us (4.2 TB/s; a copy of as many bytes 19 us); its gradient, 235 MB, 48.8 us
+// (4.8 TB/s); 4 x 2048 x 1024 fp32 22.0 and 38.1 us.  One thread per channel took 1221
+// and (padded batch) 2194 us; loads into registers one tile ahead 39.0 and 64.8 us.
+// 1 x 16384 x 1024 (N = 8): 32.0 us, of which the exchanges between CTAs, about 0.9 us
+// per round, are 7.  Odd bf16 widths, whose copies are not asynchronous, take 69 and
+// 107 instructions per value and wait for them: 8 x 2048 x 999 76 and 106 us.
 constexpr int kGrWarps = 8;
 constexpr int kGrThreads = 32 * kGrWarps;
 constexpr int kGrStages = 3;

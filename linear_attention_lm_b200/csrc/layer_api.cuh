@@ -258,13 +258,13 @@ bool launch_gatedrec(void (*kern)(P), const P& p, long long clusters, size_t sme
 
 // The cut of a recurrence: G groups of lanes per warp (64 / G channels per CTA) and N
 // CTAs per cluster, for up to two CTAs per SM.  Two groups cost less than two CTAs
-// (8 x 2048 x 1024 bf16: forward 24.2 us with G = 2, N = 1, 27.6 with G = 1, N = 2 and
-// 28.1 with neither; gradient 46.7, 58.1 and 54.4), but rows of 32 bytes (G = 4) lose
-// to eight CTAs (1 x 16384 x 1024: forward 31.4 us with G = 2, N = 8, 33.5 with G = 4,
+// (8 x 2048 x 1024 bf16: forward 24.2 us with G = 2, N = 1, 27.3 with G = 1, N = 2 and
+// 27.2 with neither; gradient 48.9, 53.7 and 55.7), but rows of 32 bytes (G = 4) lose
+// to eight CTAs (1 x 16384 x 1024: forward 31.8 us with G = 2, N = 8, 34.6 with G = 4,
 // N = 4), so G = 4 is for fewer channels than eight CTAs fill the GPU with.  A padded
 // batch leaves SMs to its longest sequences early: twice the CTAs, and G = 4 before
-// clusters (8 sequences of 0 to 2048 tokens x 1024: forward 19.6 us, gradient 35.7;
-// as for full sequences 22.4 and 44.3; G = 2, N = 2: 21.6 and 40.6).
+// clusters (8 sequences of 0 to 2048 tokens x 1024: forward 21.5 us, gradient 37.3;
+// as for full sequences 23.6 and 45.6; G = 2, N = 2: 22.2 and 41.6).
 struct GrPlan {
   int G, N, n_blk;
 };
@@ -291,10 +291,10 @@ constexpr int kGrShortBwdMostL = 48;
 
 // Whether one thread per two channels walks the sequences: they are shorter than
 // a round of tiles, or so many that the walk fills the GPU.  128 x L x 1024 bf16,
-// forward, walked and in tiles: L = 16 under 10 and 26.8 us, 64: 14.6 and 26.5,
-// 128: 27.0 and 30.1 (64 x 256 x 1024: 39.8 and 24.8); gradient: L = 16 under 9 and
-// 25.2, 48: 22.7 and 30.6, 64: 41.9 and 34.2.  Odd rows, with single loads, lose
-// beyond the shortest (128 x 128 x 999: 112 and 64 us).
+// forward, walked and in tiles: L = 16 4.3 and 26.1 us, 64: 14.3 and 26.4, 128: 25.9
+// and 29.6 (64 x 128 x 1024: 18.0 and 16.7); gradient: L = 16 8.5 and 25.5, 48: 22.6
+// and 30.9, 64: 42.1 and 34.0.  Odd rows, with single loads, lose beyond the shortest
+// (128 x 128 x 999: 90 and 64 us).
 inline bool gatedrec_short(int B, int L, int D, bool forward) {
   if (L <= 16) return true;
   if (D % 2 != 0) return false;

@@ -7,14 +7,18 @@
 //     dx = s (t - mean(t) - xh mean(t xh)) + dresid
 //     dw = sum_rows dy xh,  db = sum_rows dy
 //
-// Both are bound by HBM bandwidth: a row is read once, stays in registers for
-// its sums (the variance is summed over the centred values, so a large mean
-// costs no precision) and its outputs are written once.  All sums are fp32.
+// A row is read once, stays in registers for its sums (the variance is summed over the
+// centred values, so a large mean costs no precision) and its outputs are written
+// once.  All sums are fp32.  Rows of whole vectors are bound by HBM bandwidth; rows that
+// no vector divides by single-value accesses (74 and 78 instructions per value); the
+// gradient of rows of more than 8192 by its loads, see there.
 //
 // Measured on B200 (a plain device copy of as many bytes in brackets): forward
 // with residual, 16384 x 1024 bf16, 134 MB: 24.0 us, 5.6 TB/s (24.6 us); gradient
 // with dresid, 16384 x 2048 bf16, 403 MB: 66 us, 6.1 TB/s.  Loading one row per
-// short-lived warp, with nothing ahead, took 30.0 and 146 us.
+// short-lived warp, with nothing ahead, took 30.0 and 146 us.  Forward fp32, 16384 x
+// 1024 with residual, 268 MB: 47.4 us (44.2 us).  16384 x 999 bf16 with residual and
+// dresid: forward 60.5, gradient 58.5 us.
 #pragma once
 
 #include "common.cuh"
@@ -190,8 +194,13 @@ struct LnBwdParams {
 // copied ahead by cp.async.  Where rows are whole vectors of four, each thread
 // copies what it will read itself and no barrier is between a row's arrival and its
 // use; other rows are copied as the 16-byte pieces that hold them, by the whole
-// group (3001 x 999 fp32: 19.8 us with 4-byte copies, 15.3 with pieces; 16384 x 999
+// group (3001 x 999 fp32: 19.8 us with 4-byte copies, 15.8 with pieces; 16384 x 999
 // bf16, where two-byte copies have no asynchronous form: 148 and 59 us).
+//
+// Rows of more than 8192 values take 1024 threads, which may have 64 registers each: the
+// five arrays of 16 values do not fit (488 to 792 bytes of spill stores per thread,
+// 368 to 816 of loads) and nothing is copied ahead, so every row waits for its loads.
+// 2048 rows bf16 with dresid: width 8192 40.9 us, 12288 169, 16384 190, 16383 282.
 template <typename T, int V, int E, int kThreads>
 struct LnBwdShape {
   static constexpr int NV = E / V;

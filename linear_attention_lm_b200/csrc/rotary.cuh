@@ -7,7 +7,8 @@
 // or (2i, 2i+1) ("interleaved"); values from rot on pass through.
 //
 // Angles: p f_i is formed in fp64 and its whole turns are taken off before it
-// becomes fp32, so positions up to 2^31 keep about 2^-24 of a turn.
+// becomes fp32, so positions up to 2^31 keep about 2^-24 of a turn.  Sine and cosine
+// are fp32, and their products with an m that is not a power of two are rounded too.
 //
 // Bound by HBM bandwidth (every value read and written once).  A thread owns V
 // pairs of one position and walks the heads, queries' and then keys', so that
