@@ -21,7 +21,7 @@ constexpr int kGrChunk = 64;  // tokens between two saved states
 // exponent, which grows with |g|, and that of the product; beyond |g| = 87 it is 0.
 //
 // Just below 1 fp32 has steps of 2^-24, so a alone would hold a slow decay's rate n only
-// to 2^-25 (0.07% at a logit of 10, up to half at 16), the same way at every token of a
+// to 2^-25 (0.07% at a logit of 10, up to a quarter at 16), the same way at every token of a
 // constant gate.  What decays a state takes the rate from n instead: the map of a lane's
 // tokens by map_kept, the walk token by token by gate_rest.  What stays is the rounding
 // of the fp32 state itself, at each update.
