@@ -308,9 +308,10 @@ based_status_t based_baseconv_fwd(const void* x, const void* w, const float* bia
  * The norm is that of the stream as it is stored (rounded), so the gradient of
  * the stored stream is the gradient of this call.  eps > 0, 1 <= D <= 16384
  * (else BASED_ERR_UNSUPPORTED), any number of rows.  The sums are fp32: a row's
- * sum, and the sum of the squares of r - m, have to stay below 3.4e38 (they do for
- * |r| <= 7e16; a row past that gives y = bias, infinity or NaN).  In place: resid_out may be
- * x or residual, and y may be the other of them (or x); no other overlap.
+ * sum, and the sum of the squares of r - m, have to stay below 3.4e38 (they do
+ * for |r| <= 7e16; a row past that gives y = bias, infinity or NaN).
+ * In place: resid_out may be x or residual, and y may be the other of them (or
+ * x); no other overlap.
  */
 based_status_t based_layernorm_fwd(const void* x, const void* residual, const float* weight,
                                    const float* bias, void* y, void* resid_out, float* mean,
